@@ -66,7 +66,9 @@ typedef enum nvfp4_status {
   NVFP4_E_ARCH = 5,           /* device is not compute capability 10.3       */
   NVFP4_E_CUDA = 6,           /* a CUDA runtime/driver call failed           */
   NVFP4_E_DEVICE_TIMEOUT = 7, /* (device) a bounded wait ran out             */
-  NVFP4_E_BAD_ROUTING = 8     /* (device) inconsistent expert offsets / ids  */
+  NVFP4_E_BAD_ROUTING = 8,    /* (device) inconsistent expert offsets / ids  */
+  NVFP4_E_CACHE_FULL = 9,     /* (device) no free page or table column left  */
+  NVFP4_E_BAD_PAGE = 10       /* (device) page id, slot or length out of range */
 } nvfp4_status;
 
 enum { NVFP4_DT_BF16 = 0, NVFP4_DT_F32 = 1 };
@@ -509,6 +511,135 @@ int moe_align_permute_noalloc(const float* logits, int T, int E, int k, int32_t*
                               int32_t* expert_offsets, int32_t* perm, int32_t* inv, int act_kind, const void* act_in,
                               const uint8_t* act_in_scales, int64_t act_cols, void* act_out,
                               uint8_t* act_out_scales, int32_t* dev_status, nvfp4_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * The decoder block around the layer: a paged key/value cache held in 8 bits
+ * (kv_plan, kv_append, kv_attention) and the norms between the blocks and the
+ * residual stream (block_norm).  The pages define no such step: they run the
+ * layer inside a decoder whose attention they do not describe, so formats and
+ * formulas are this library's own.
+ *
+ * Cache: one half for keys and one for values, each
+ *   codes  uint8 [P, Hkv, S, D]  E4M3 codes; P pages (blocks) of S tokens
+ *   exps   uint8 [P, Hkv]        UE8M0 block scales (as MXFP4's)
+ * and value = e4m3(code) * 2^(exp - 127).  A power of two loses nothing
+ * against an fp32 scale inside E4M3's normal range, and lets a block take a
+ * larger scale later with one rounding of the codes that fall below it.
+ * S is 16, 32, 64 or 128; D is 64 or 128.  A page belongs to one request; row
+ * b of the block table int32 [B, M] (row stride ld_table) lists request b's
+ * pages in order.  Token position p of b is slot page * S + p % S of page
+ * table[b][p / S] (P * S <= 2^31 - 1).  Entries of the table past a request's
+ * length are never used.
+ * ------------------------------------------------------------------------ */
+
+/* ------------------------------------------------------------------------
+ * kv_plan -- block tables and slot maps from request lengths, for a step in
+ * which request b has ctx_lens[b] cached tokens and brings new_lens[b].
+ *   need(b)  = ceil((ctx + new) / S) - ceil(ctx / S)  pages, taken in request
+ *              order from the end of free_pages[0 .. *free_count)
+ *   fits(b)  : the pages that b and the requests before it need are there,
+ *              and ceil((ctx + new) / S) <= M
+ *   block_table  in/out: new pages are entered behind the old ones
+ *   query_start  out int32 [B + 1]: exclusive sum of new_lens
+ *   kv_lens      out int32 [B]: ctx + new (ctx where b does not fit)
+ *   slot_map     out int32 [T]: the slot of every new token in request order;
+ *                -1 for a request that does not fit and past the last token
+ *   free_left    out int32 [1]: *free_count less the pages taken (it must not
+ *                be free_count itself: two words used in turn)
+ *   num_free     entries of free_pages; *free_count is cut to [0, num_free]
+ *   dev_status   optional: NVFP4_E_CACHE_FULL if a request does not fit,
+ *                NVFP4_E_BAD_PAGE for a negative length or more than T tokens
+ *                (such a request brings no token; tokens past T get no slot)
+ * A call changes nothing that it reads, apart from table entries that a second
+ * call would fill alike: repeated, it gives the same.
+ * Constraints: 0 <= B <= 8192, T >= 0, M >= 1, ld_table >= M.
+ * ------------------------------------------------------------------------ */
+int kv_plan(const int32_t* ctx_lens, const int32_t* new_lens, int B, int page_size, int32_t* block_table,
+            int64_t ld_table, int M, const int32_t* free_pages, int num_free, const int32_t* free_count, int T,
+            int32_t* query_start, int32_t* kv_lens, int32_t* slot_map, int32_t* free_left, int32_t* dev_status,
+            nvfp4_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * kv_append -- new key and value rows into the cache.
+ * A run is a maximal sequence of tokens with slots s, s+1, ... inside one
+ * page (what kv_plan gives); a page has one run in a call.  For every run,
+ * head and half, o = s % S:
+ *   e    = smallest integer with amax(|x|) <= 448 * 2^e over the run (NaN not
+ *          counted, an infinity as the largest finite fp32, zeros as -127),
+ *          in [-127, 127]; for o > 0 at least the block's old exponent e0
+ *   codes of positions 0 .. o-1: E4M3(value * 2^(e0 - e)), one rounding; not
+ *          touched when e == e0
+ *   codes of the new rows: E4M3(x * 2^-e) (round to nearest even, saturating
+ *          at 448; NaN stays NaN)
+ *   exps[page, head] = e + 127
+ *   k, v        [T, Hkv, D] of x_dtype (NVFP4_DT_BF16 or NVFP4_DT_F32), token
+ *               strides ld_k, ld_v elements (slices of one projection's output
+ *               need no copy)
+ *   slot_map    int32 [T]; a negative slot is skipped
+ *   dev_status  optional: NVFP4_E_BAD_PAGE for a slot past the cache (skipped)
+ * Constraints: ld >= Hkv * D and ld % 8 == 0 (bf16) or % 4 == 0 (f32).
+ * ------------------------------------------------------------------------ */
+int kv_append(const void* k, const void* v, int x_dtype, int64_t ld_k, int64_t ld_v, const int32_t* slot_map, int T,
+              int Hkv, int D, int64_t num_pages, int page_size, uint8_t* k_codes, uint8_t* k_exps, uint8_t* v_codes,
+              uint8_t* v_exps, int32_t* dev_status, nvfp4_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * kv_attention -- attention of the new tokens' queries over the cache.
+ * Query i of request b (token query_start[b] + i of n = query_start[b+1] -
+ * query_start[b]) sees the keys j < kv_lens[b] - n + i + 1.  With K/V head
+ * h / (Hq / Hkv) for query head h:
+ *   s_j = scale * sum_d q[d] * k_j[d];   lse = ln sum_j exp(s_j)
+ *   out = sum_j exp(s_j - lse) * v_j
+ * A row that sees no key gets out = 0 and lse = -inf.  One token, a few
+ * drafted tokens and prompt chunks may be mixed in one call.
+ *   q      bf16 [T, Hq, D], token stride ld_q elements
+ *   out    bf16 [T, Hq, D]; lse optional fp32 [T, Hq]
+ *   query_start int32 [B + 1], kv_lens int32 [B] (as kv_plan gives them)
+ *   max_query_len  an upper bound of n that chooses the kernels; a longer
+ *          request is still computed
+ *   workspace  >= kv_attention_workspace_bytes(T, B, Hq, Hkv, D) bytes (for
+ *          the current device)
+ *   dev_status  optional: NVFP4_E_BAD_PAGE for a page outside the cache, a
+ *          length past the table or query_start outside [0, T] (keys of such
+ *          a page count as not there, lengths and rows are cut);
+ *          NVFP4_E_DEVICE_TIMEOUT if a bounded wait ran out
+ * A sum that would lose against the largest value block of the request is
+ * rounded relative to that block.  A NaN code of a value reaches every query
+ * of its request and call.  Rows of out past query_start[B] are not written.
+ * The result does not depend on the other requests of the call, except that
+ * their lengths move the points at which partial sums are joined.
+ * Constraints: Hq % Hkv == 0, ld_q >= Hq * D, ld_q % 8 == 0, M >= 1,
+ * 0 <= B <= 8192.
+ * ------------------------------------------------------------------------ */
+size_t kv_attention_workspace_bytes(int T, int B, int Hq, int Hkv, int D);
+int kv_attention(const void* q, int64_t ld_q, const uint8_t* k_codes, const uint8_t* k_exps, const uint8_t* v_codes,
+                 const uint8_t* v_exps, const int32_t* block_table, int64_t ld_table, int M, const int32_t* kv_lens,
+                 const int32_t* query_start, int T, int B, int Hq, int Hkv, int D, int64_t num_pages, int page_size,
+                 int max_query_len, float scale, void* out, float* lse, int32_t* dev_status, void* workspace,
+                 size_t workspace_bytes, nvfp4_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * block_norm -- the norms after one block and before the next, with the
+ * block's gate, its residual scale and the residual addition between them:
+ *   u = a * rsqrt(mean(a^2) + eps) * w_post       (u = a without w_post)
+ *   y = x + alpha * gate * u                      (y = x without a)
+ *   h = y * rsqrt(mean(y^2) + eps) * w_pre        (not written without w_pre)
+ * in fp32 (h from y before y's rounding), one pass over the data.
+ *   x    bf16 [T, H], row stride ld_x: the residual stream
+ *   a    optional [T, H] of a_dtype (NVFP4_DT_F32, as moe_layer_forward and
+ *        moe_combine give it, or NVFP4_DT_BF16), row stride ld_a
+ *   gate optional bf16: element (t, c) at t * gate_ld_t + c * gate_ld_c;
+ *        gate_ld_c is 0 (one value for a token) or 1, gate_ld_t 0 (the same
+ *        for every token) or the row stride
+ *   w_post, w_pre  optional bf16 [H]
+ *   y    out bf16 [T, H] (required with a, unused without; may be x itself)
+ *   h    out bf16 [T, H] (required with w_pre)
+ * Constraints: H % 8 == 0, H <= 16384; row strides % 8 == 0 (bf16) or % 4 == 0
+ * (f32); gate_ld_t % 8 == 0 where gate_ld_c is 1.
+ * ------------------------------------------------------------------------ */
+int block_norm(const void* x, int64_t ld_x, const void* a, int a_dtype, int64_t ld_a, const void* gate,
+               int64_t gate_ld_t, int64_t gate_ld_c, const void* w_post, const void* w_pre, float alpha, float eps,
+               int T, int H, void* y, void* h, nvfp4_stream_t stream);
 
 #ifdef __cplusplus
 }

@@ -20,7 +20,8 @@ NVFP4_SCALE_STATIC, NVFP4_SCALE_DYNAMIC = 0, 1
 MOE_W4A4, MOE_W4A16, MOE_MXW4A4, MOE_W4A8, MOE_W4A16F = 0, 1, 2, 3, 4
 MOE_ACT_NONE, MOE_ACT_NVFP4, MOE_ACT_BF16 = 0, 1, 2
 STATUS_NAMES = {0: "NVFP4_OK", 1: "NVFP4_E_INVAL", 2: "NVFP4_E_SHAPE", 3: "NVFP4_E_ALIGN", 4: "NVFP4_E_WORKSPACE",
-                5: "NVFP4_E_ARCH", 6: "NVFP4_E_CUDA", 7: "NVFP4_E_DEVICE_TIMEOUT", 8: "NVFP4_E_BAD_ROUTING"}
+                5: "NVFP4_E_ARCH", 6: "NVFP4_E_CUDA", 7: "NVFP4_E_DEVICE_TIMEOUT", 8: "NVFP4_E_BAD_ROUTING",
+                9: "NVFP4_E_CACHE_FULL", 10: "NVFP4_E_BAD_PAGE"}
 
 # every symbol the header declares, in declaration order
 EXPORTS = ("nvfp4_status_string", "nvfp4_device_check", "nvfp4_quantize_workspace_bytes", "nvfp4_quantize",
@@ -31,7 +32,7 @@ EXPORTS = ("nvfp4_status_string", "nvfp4_device_check", "nvfp4_quantize_workspac
            "moe_router_logits_workspace_bytes", "moe_router_logits", "moe_layer_host_workspace_bytes",
            "moe_layer_forward_host", "fp8_quantize", "moe_route_quantize_fp8", "moe_router_route_workspace_bytes",
            "moe_router_route", "moe_gather_f16", "moe_swiglu_f16", "moe_route_quantize_fp8_f16",
-           "moe_swiglu_fp8_f16")
+           "moe_swiglu_fp8_f16", "kv_plan", "kv_append", "kv_attention_workspace_bytes", "kv_attention", "block_norm")
 
 
 class Nvfp4Error(RuntimeError):
@@ -42,7 +43,7 @@ class Nvfp4Error(RuntimeError):
 
 _lib = None
 
-_P, _I, _I64, _SZ = C.c_void_p, C.c_int, C.c_int64, C.c_size_t
+_P, _I, _I64, _SZ, _F = C.c_void_p, C.c_int, C.c_int64, C.c_size_t, C.c_float
 
 
 def library_path() -> str:
@@ -121,6 +122,17 @@ def load(build_if_missing: bool = True):
     L.fp8_quantize.argtypes = [_P, _I, _I64, _I64, _I64, _P, _I, _P, _P, _SZ, _P]
     L.moe_route_quantize_fp8.restype = _I
     L.moe_route_quantize_fp8.argtypes = [_P, _P, _I, _I, _I, _I, _P, _P, _P, _P, _P, _P, _P, _P, _P, _SZ, _P]
+    L.kv_plan.restype = _I
+    L.kv_plan.argtypes = [_P, _P, _I, _I, _P, _I64, _I, _P, _I, _P, _I, _P, _P, _P, _P, _P, _P]
+    L.kv_append.restype = _I
+    L.kv_append.argtypes = [_P, _P, _I, _I64, _I64, _P, _I, _I, _I, _I64, _I, _P, _P, _P, _P, _P, _P]
+    L.kv_attention_workspace_bytes.restype = _SZ
+    L.kv_attention_workspace_bytes.argtypes = [_I, _I, _I, _I, _I]
+    L.kv_attention.restype = _I
+    L.kv_attention.argtypes = [_P, _I64, _P, _P, _P, _P, _P, _I64, _I, _P, _P, _I, _I, _I, _I, _I, _I64, _I, _I, _F,
+                               _P, _P, _P, _P, _SZ, _P]
+    L.block_norm.restype = _I
+    L.block_norm.argtypes = [_P, _I64, _P, _I, _I64, _P, _I64, _I64, _P, _P, _F, _F, _I, _I, _P, _P, _P]
     _lib = L
     return L
 
@@ -548,6 +560,185 @@ def moe_layer_forward_host(mode, x_host, logits_host, k, w13, w2, S_h, out_host=
                                     _hptr(out_host), _ptr(dev_status), _ptr(workspace), workspace.numel(),
                                     _stream()))
     return out_host
+
+
+# ---------------------------------------------------------------------------
+# the decoder block around the layer: paged 8-bit KV cache, attention, norms
+# ---------------------------------------------------------------------------
+
+# Host time of these calls matters (a decode step makes several, each a few
+# microseconds of GPU work), so the checks read every attribute once.
+
+_U8, _I32, _BF16, _F32 = torch.uint8, torch.int32, torch.bfloat16, torch.float32
+
+
+def _addr(t):
+    if not t.is_cuda:
+        raise ValueError("expected a CUDA tensor")
+    return t.data_ptr()
+
+
+def _opt(t):
+    return None if t is None else _addr(t)
+
+
+def _raw_stream(t):
+    """The current stream of t's device, as a handle."""
+    return torch._C._cuda_getCurrentRawStream(t.get_device())
+
+
+def _is(t, dtype, shape):
+    return t.dtype == dtype and t.shape == shape and t.is_contiguous()
+
+
+def _refuse(what):
+    raise ValueError(what)
+
+
+def _cache_dims(k_codes, k_exps, v_codes, v_exps):
+    shape = k_codes.shape
+    if len(shape) != 4 or not (_is(k_codes, _U8, shape) and _is(v_codes, _U8, shape) and _is(k_exps, _U8, shape[:2]) and
+                               _is(v_exps, _U8, shape[:2])):
+        _refuse("the cache must be contiguous uint8: codes [P, Hkv, S, D] and exps [P, Hkv], keys and values alike")
+    return shape
+
+
+def _head_rows(x, T, H, D, name):
+    """Token stride of x [T, H, D] with contiguous tokens."""
+    st = x.stride()
+    if x.shape != (T, H, D) or st[2] != 1 or (st[1] != D and H > 1):
+        _refuse("%s must be [%d, %d, %d] with contiguous tokens" % (name, T, H, D))
+    return st[0] if T > 1 else H * D
+
+
+def _matrix_rows(x, T, H, name):
+    """Row stride of x [T, H] with contiguous rows."""
+    st = x.stride()
+    if x.shape != (T, H) or (st[1] != 1 and H > 1):
+        _refuse("%s must be [%d, %d] with contiguous rows" % (name, T, H))
+    return st[0] if T > 1 else H
+
+
+def _table_dims(block_table, B):
+    if block_table.dtype != _I32 or block_table.dim() != 2:
+        _refuse("block_table must be int32 [B, M]")
+    M = block_table.shape[1]
+    return _matrix_rows(block_table, B, M, "block_table"), M
+
+
+def kv_plan(ctx_lens, new_lens, block_table, free_pages, free_count, page_size, T, dev_status=None):
+    """Pages and slots of a step's new tokens.  ctx_lens, new_lens int32 [B],
+    block_table int32 [B, M] (new pages are entered in place), free_pages
+    int32 [N] of which the first free_count (int32 [1]) are free.  Returns
+    dict(query_start [B+1], kv_lens [B], slot_map [T], free_left [1])."""
+    L = load()
+    B, N = ctx_lens.numel(), free_pages.numel()
+    if not (_is(ctx_lens, _I32, (B,)) and _is(new_lens, _I32, (B,)) and _is(free_pages, _I32, (N,)) and
+            _is(free_count, _I32, (1,))):
+        _refuse("ctx_lens, new_lens [B], free_pages [N] and free_count [1] must be contiguous int32")
+    ld, M = _table_dims(block_table, B)
+    # one allocation, each part on a 16-byte boundary
+    n0, n1, n2 = (B + 4) & -4, (B + 3) & -4, (T + 3) & -4
+    buf = _empty((n0 + n1 + n2 + 4,), _I32, ctx_lens.device)
+    start, _, kv, _, slots, _, left, _ = buf.split_with_sizes((B + 1, n0 - B - 1, B, n1 - B, T, n2 - T, 1, 3))
+    p = buf.data_ptr()
+    _check("kv_plan", L.kv_plan(_addr(ctx_lens), _addr(new_lens), B, page_size, _addr(block_table), ld, M,
+                                _addr(free_pages), N, _addr(free_count), T, p, p + 4 * n0, p + 4 * (n0 + n1),
+                                p + 4 * (n0 + n1 + n2), _opt(dev_status), _raw_stream(ctx_lens)))
+    return dict(query_start=start, kv_lens=kv, slot_map=slots, free_left=left)
+
+
+def kv_append(k, v, slot_map, k_codes, k_exps, v_codes, v_exps, dev_status=None):
+    """New rows k, v [T, Hkv, D] (bf16 or fp32; tokens contiguous, any token
+    stride) into the cache's slots slot_map int32 [T], in place."""
+    L = load()
+    P, Hkv, S, D = _cache_dims(k_codes, k_exps, v_codes, v_exps)
+    T = slot_map.numel()
+    dt = k.dtype
+    if not _is(slot_map, _I32, (T,)) or v.dtype != dt or (dt != _BF16 and dt != _F32):
+        _refuse("slot_map must be contiguous int32 [T], k and v both bf16 or both fp32")
+    _check("kv_append", L.kv_append(_addr(k), _addr(v), NVFP4_DT_BF16 if dt == _BF16 else NVFP4_DT_F32,
+                                    _head_rows(k, T, Hkv, D, "k"), _head_rows(v, T, Hkv, D, "v"), _addr(slot_map), T,
+                                    Hkv, D, P, S, _addr(k_codes), _addr(k_exps), _addr(v_codes), _addr(v_exps),
+                                    _opt(dev_status), _raw_stream(k)))
+
+
+def kv_attention_workspace_bytes(T, B, Hq, Hkv, D):
+    return int(load().kv_attention_workspace_bytes(T, B, Hq, Hkv, D))
+
+
+def kv_attention(q, k_codes, k_exps, v_codes, v_exps, block_table, kv_lens, query_start, max_query_len, scale=None,
+                 out=None, want_lse=False, dev_status=None, workspace=None):
+    """Attention of q [T, Hq, D] bf16 (any token stride) over the cached keys
+    and values of each query's request.  scale=None: D ** -0.5.  Returns out
+    [T, Hq, D] bf16, or (out, lse [T, Hq] fp32)."""
+    L = load()
+    P, Hkv, S, D = _cache_dims(k_codes, k_exps, v_codes, v_exps)
+    if q.dim() != 3 or q.dtype != _BF16:
+        _refuse("q must be bf16 [T, Hq, D]")
+    T, Hq, _ = q.shape
+    B = kv_lens.numel()
+    ld_q = _head_rows(q, T, Hq, D, "q")
+    if not (_is(kv_lens, _I32, (B,)) and _is(query_start, _I32, (B + 1,))):
+        _refuse("kv_lens [B] and query_start [B + 1] must be contiguous int32")
+    ld_t, M = _table_dims(block_table, B)
+    if out is None:
+        out = _empty((T, Hq, D), _BF16, q.device)
+    elif not _is(out, _BF16, (T, Hq, D)):
+        _refuse("out must be contiguous bf16 [T, Hq, D]")
+    lse = _empty((T, Hq), _F32, q.device) if want_lse else None
+    if workspace is None:
+        workspace = _empty(kv_attention_workspace_bytes(T, B, Hq, Hkv, D), _U8, q.device)
+    _check("kv_attention",
+           L.kv_attention(_addr(q), ld_q, _addr(k_codes), _addr(k_exps), _addr(v_codes), _addr(v_exps),
+                          _addr(block_table), ld_t, M, _addr(kv_lens), _addr(query_start), T, B, Hq, Hkv, D, P, S,
+                          max_query_len, D ** -0.5 if scale is None else scale, _addr(out), _opt(lse),
+                          _opt(dev_status), _addr(workspace), workspace.numel() * workspace.element_size(),
+                          _raw_stream(q)))
+    return (out, lse) if want_lse else out
+
+
+def block_norm(x, a=None, gate=None, w_post=None, w_pre=None, alpha=1.0, eps=1e-6, y=None):
+    """y = x + alpha * gate * norm(a) * w_post and h = norm(y) * w_pre for x
+    [T, H] bf16 and a [T, H] fp32 or bf16.  gate: bf16, one of [H], [1, H],
+    [T, 1] or [T, H].  y: where to write it (x itself will do).  Returns
+    (y, h); y is x without a, h is None without w_pre."""
+    L = load()
+    if x.dim() != 2 or x.dtype != _BF16:
+        _refuse("x must be bf16 [T, H]")
+    T, H = x.shape
+    ld_x = _matrix_rows(x, T, H, "x")
+    dt, ld_a, y_out = NVFP4_DT_F32, 0, None
+    g_t = g_c = 0
+    if a is None:
+        if gate is not None or w_post is not None or y is not None:
+            _refuse("gate, w_post and y belong to a")
+        y = x
+    else:
+        if a.dtype == _BF16:
+            dt = NVFP4_DT_BF16
+        elif a.dtype != _F32:
+            _refuse("a must be bf16 or fp32")
+        ld_a = _matrix_rows(a, T, H, "a")
+        if y is None:
+            y = _empty((T, H), _BF16, x.device)
+        elif not _is(y, _BF16, (T, H)):
+            _refuse("y must be contiguous bf16 [T, H]")
+        y_out = _addr(y)
+    if gate is not None:
+        if gate.dim() == 1:
+            gate = gate[None]
+        n, m = gate.shape
+        if gate.dtype != _BF16 or n not in (1, T) or m not in (1, H):
+            _refuse("gate must be bf16 [H], [1, H], [T, 1] or [T, H]")
+        st = gate.stride()
+        g_t, g_c = st[0] if n > 1 else 0, st[1] if m > 1 else 0
+    if (w_post is not None and not _is(w_post, _BF16, (H,))) or (w_pre is not None and not _is(w_pre, _BF16, (H,))):
+        _refuse("w_post and w_pre must be contiguous bf16 [H]")
+    h = _empty((T, H), _BF16, x.device) if w_pre is not None else None
+    _check("block_norm", L.block_norm(_addr(x), ld_x, _opt(a), dt, ld_a, _opt(gate), g_t, g_c, _opt(w_post),
+                                      _opt(w_pre), alpha, eps, T, H, y_out, _opt(h), _raw_stream(x)))
+    return y, h
 
 
 class MoELayerGraph:

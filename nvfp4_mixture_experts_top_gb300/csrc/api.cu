@@ -53,7 +53,7 @@ int num_sms() {
 // cudaFuncAttributeMaxDynamicSharedMemorySize for `func` on the current
 // device, set once per (kernel, device): a process may drive several GPUs.
 cudaError_t ensure_dynamic_smem(const void* func, int bytes) {
-  constexpr int kFuncs = 16;
+  constexpr int kFuncs = 32;
   static const void* funcs[kFuncs];
   static bool done[kFuncs][kMaxDevices];
   const int d = current_device();
@@ -111,6 +111,8 @@ const char* nvfp4_status_string(int status) {
     case NVFP4_E_CUDA: return "NVFP4_E_CUDA: a CUDA call failed";
     case NVFP4_E_DEVICE_TIMEOUT: return "NVFP4_E_DEVICE_TIMEOUT: a bounded device wait ran out";
     case NVFP4_E_BAD_ROUTING: return "NVFP4_E_BAD_ROUTING: inconsistent expert offsets or ids";
+    case NVFP4_E_CACHE_FULL: return "NVFP4_E_CACHE_FULL: no free page or table column left";
+    case NVFP4_E_BAD_PAGE: return "NVFP4_E_BAD_PAGE: a page id, slot or length is out of range";
     default: return "unknown nvfp4_status";
   }
 }
@@ -735,6 +737,106 @@ int moe_layer_forward_host(int mode, const void* x_host, const float* logits_hos
   return moe_layer_forward(mode, x_dev, lg_dev, T, H, I, E, k, w13_codes, w13_scales_packed, w13_S, w2_codes,
                            w2_scales_packed, w2_S, S_h, static_cast<float*>(od), dev_status, workspace, layer_bytes,
                            stream);
+}
+
+static bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+static bool page_size_ok(int S) { return S == 16 || S == 32 || S == 64 || S == 128; }
+
+int kv_plan(const int32_t* ctx_lens, const int32_t* new_lens, int B, int page_size, int32_t* block_table,
+            int64_t ld_table, int M, const int32_t* free_pages, int num_free, const int32_t* free_count, int T,
+            int32_t* query_start, int32_t* kv_lens, int32_t* slot_map, int32_t* free_left, int32_t* dev_status,
+            nvfp4_stream_t stream) {
+  if (B < 0 || T < 0 || M < 0 || num_free < 0) return NVFP4_E_INVAL;
+  if (!page_size_ok(page_size) || B > kMaxKvRequests || M < 1 || ld_table < M) return NVFP4_E_SHAPE;
+  if (free_count == nullptr || query_start == nullptr || free_left == nullptr || free_left == free_count)
+    return NVFP4_E_INVAL;
+  if (B > 0 && (ctx_lens == nullptr || new_lens == nullptr || block_table == nullptr || kv_lens == nullptr))
+    return NVFP4_E_INVAL;
+  if ((T > 0 && slot_map == nullptr) || (num_free > 0 && free_pages == nullptr)) return NVFP4_E_INVAL;
+  if (!aligned4(ctx_lens) || !aligned4(new_lens) || !aligned4(block_table) || !aligned4(free_pages) ||
+      !aligned4(free_count) || !aligned4(query_start) || !aligned4(kv_lens) || !aligned4(slot_map) ||
+      !aligned4(free_left) || !aligned4(dev_status))
+    return NVFP4_E_ALIGN;
+  CHECK_ARCH();
+  return cuda_status(launch_kv_plan(ctx_lens, new_lens, B, page_size, block_table, ld_table, M, free_pages, num_free,
+                                    free_count, T, query_start, kv_lens, slot_map, free_left, dev_status,
+                                    reinterpret_cast<cudaStream_t>(stream)));
+}
+
+int kv_append(const void* k, const void* v, int x_dtype, int64_t ld_k, int64_t ld_v, const int32_t* slot_map, int T,
+              int Hkv, int D, int64_t num_pages, int page_size, uint8_t* k_codes, uint8_t* k_exps, uint8_t* v_codes,
+              uint8_t* v_exps, int32_t* dev_status, nvfp4_stream_t stream) {
+  if (T < 0 || Hkv <= 0 || num_pages < 0) return NVFP4_E_INVAL;
+  if (x_dtype != NVFP4_DT_BF16 && x_dtype != NVFP4_DT_F32) return NVFP4_E_INVAL;
+  if ((D != 64 && D != 128) || !page_size_ok(page_size) || num_pages > INT32_MAX / page_size) return NVFP4_E_SHAPE;
+  const int64_t row = (int64_t)Hkv * D, unit = x_dtype == NVFP4_DT_BF16 ? 8 : 4;
+  if (ld_k < row || ld_v < row || ld_k % unit != 0 || ld_v % unit != 0) return NVFP4_E_SHAPE;
+  if (T == 0) return NVFP4_OK;
+  if (k == nullptr || v == nullptr || slot_map == nullptr || k_codes == nullptr || k_exps == nullptr ||
+      v_codes == nullptr || v_exps == nullptr)
+    return NVFP4_E_INVAL;
+  if (!aligned16(k) || !aligned16(v) || !aligned16(k_codes) || !aligned16(v_codes) || !aligned4(slot_map) ||
+      !aligned4(dev_status))
+    return NVFP4_E_ALIGN;
+  CHECK_ARCH();
+  return cuda_status(launch_kv_append(k, v, x_dtype, ld_k, ld_v, slot_map, T, Hkv, D, num_pages, page_size, k_codes,
+                                      k_exps, v_codes, v_exps, dev_status, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+size_t kv_attention_workspace_bytes(int T, int B, int Hq, int Hkv, int D) {
+  if (T < 0 || B < 0 || Hq <= 0 || Hkv <= 0 || D <= 0) return 0;
+  return kv_attention_ws_bytes(T, B, Hq, Hkv, D);
+}
+
+int kv_attention(const void* q, int64_t ld_q, const uint8_t* k_codes, const uint8_t* k_exps, const uint8_t* v_codes,
+                 const uint8_t* v_exps, const int32_t* block_table, int64_t ld_table, int M, const int32_t* kv_lens,
+                 const int32_t* query_start, int T, int B, int Hq, int Hkv, int D, int64_t num_pages, int page_size,
+                 int max_query_len, float scale, void* out, float* lse, int32_t* dev_status, void* workspace,
+                 size_t workspace_bytes, nvfp4_stream_t stream) {
+  if (T < 0 || B < 0 || Hq <= 0 || Hkv <= 0 || M < 0 || num_pages < 0 || max_query_len < 0) return NVFP4_E_INVAL;
+  if ((D != 64 && D != 128) || !page_size_ok(page_size) || Hq % Hkv != 0 || B > kMaxKvRequests || M < 1 ||
+      ld_table < M || num_pages > INT32_MAX / page_size)
+    return NVFP4_E_SHAPE;
+  if (ld_q < (int64_t)Hq * D || ld_q % 8 != 0) return NVFP4_E_SHAPE;
+  if (T == 0 || B == 0) return NVFP4_OK;
+  if (q == nullptr || k_codes == nullptr || k_exps == nullptr || v_codes == nullptr || v_exps == nullptr ||
+      block_table == nullptr || kv_lens == nullptr || query_start == nullptr || out == nullptr)
+    return NVFP4_E_INVAL;
+  if (!aligned16(q) || !aligned16(k_codes) || !aligned16(v_codes) || !aligned16(out) || !aligned4(block_table) ||
+      !aligned4(kv_lens) || !aligned4(query_start) || !aligned4(lse) || !aligned4(dev_status))
+    return NVFP4_E_ALIGN;
+  if (workspace == nullptr || workspace_bytes < kv_attention_workspace_bytes(T, B, Hq, Hkv, D))
+    return NVFP4_E_WORKSPACE;
+  if (!aligned16(workspace)) return NVFP4_E_ALIGN;
+  CHECK_ARCH();
+  const KvAttention a = {q, ld_q, k_codes, k_exps, v_codes, v_exps, block_table, ld_table, M, kv_lens, query_start,
+                         T, B, Hq, Hkv, D, num_pages, page_size, max_query_len, scale, out, lse, dev_status, workspace};
+  return cuda_status(launch_kv_attention(a, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+int block_norm(const void* x, int64_t ld_x, const void* a, int a_dtype, int64_t ld_a, const void* gate,
+               int64_t gate_ld_t, int64_t gate_ld_c, const void* w_post, const void* w_pre, float alpha, float eps,
+               int T, int H, void* y, void* h, nvfp4_stream_t stream) {
+  if (T < 0 || H <= 0) return NVFP4_E_INVAL;
+  if (a_dtype != NVFP4_DT_F32 && a_dtype != NVFP4_DT_BF16) return NVFP4_E_INVAL;
+  if (H % 8 != 0 || H > 16384 || ld_x < H || ld_x % 8 != 0) return NVFP4_E_SHAPE;
+  if (a != nullptr && (ld_a < H || ld_a % (a_dtype == NVFP4_DT_BF16 ? 8 : 4) != 0)) return NVFP4_E_SHAPE;
+  if (gate != nullptr) {
+    if (gate_ld_c != 0 && gate_ld_c != 1) return NVFP4_E_SHAPE;
+    if (gate_ld_t < 0 || (gate_ld_c == 1 && gate_ld_t != 0 && (gate_ld_t < H || gate_ld_t % 8 != 0)))
+      return NVFP4_E_SHAPE;
+  }
+  if (T == 0) return NVFP4_OK;
+  if (x == nullptr || (a == nullptr && w_pre == nullptr) || (a != nullptr && y == nullptr) ||
+      (w_pre != nullptr && h == nullptr))
+    return NVFP4_E_INVAL;
+  if (!aligned16(x) || !aligned16(a) || !aligned16(w_post) || !aligned16(w_pre) || !aligned16(y) || !aligned16(h) ||
+      (gate_ld_c == 1 && !aligned16(gate)) || (reinterpret_cast<uintptr_t>(gate) & 1u) != 0)
+    return NVFP4_E_ALIGN;
+  CHECK_ARCH();
+  return cuda_status(launch_block_norm(x, ld_x, a, a_dtype, ld_a, gate, gate_ld_t, gate_ld_c, w_post, w_pre, alpha,
+                                       eps, T, H, y, h, reinterpret_cast<cudaStream_t>(stream)));
 }
 
 }  // extern "C"

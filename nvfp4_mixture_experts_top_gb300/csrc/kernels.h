@@ -176,4 +176,42 @@ cudaError_t launch_gemm_mxw4a4(const uint8_t* a_codes, const uint8_t* a_scales, 
                                const uint8_t* w_scales_packed, const int32_t* offsets, int E, int N, int K, int R,
                                float* out, int32_t* dev_status, cudaStream_t st, bool early = false);
 
+// ---------------------------------------------------------------------------
+// paged 8-bit key/value cache and the norms around the blocks
+// ---------------------------------------------------------------------------
+
+constexpr int kMaxKvRequests = 8192;  // requests of a kv_plan or kv_attention call
+
+cudaError_t launch_kv_plan(const int32_t* ctx, const int32_t* add, int B, int page_size, int32_t* table,
+                           int64_t ld_table, int M, const int32_t* free_pages, int num_free,
+                           const int32_t* free_count, int T, int32_t* query_start, int32_t* kv_lens,
+                           int32_t* slot_map, int32_t* free_left, int32_t* dev_status, cudaStream_t st);
+cudaError_t launch_kv_append(const void* k, const void* v, int x_dtype, int64_t ld_k, int64_t ld_v,
+                             const int32_t* slots, int T, int Hkv, int D, int64_t num_pages, int page_size,
+                             uint8_t* k_codes, uint8_t* k_exps, uint8_t* v_codes, uint8_t* v_exps,
+                             int32_t* dev_status, cudaStream_t st);
+// Arguments of kv_attention (see the header), checked by the entry point.
+struct KvAttention {
+  const void* q;
+  int64_t ld_q;
+  const uint8_t *k_codes, *k_exps, *v_codes, *v_exps;
+  const int32_t* table;
+  int64_t ld_table;
+  int M;
+  const int32_t *kv_lens, *query_start;
+  int T, B, Hq, Hkv, D;
+  int64_t num_pages;
+  int page_size, max_query_len;
+  float scale;
+  void* out;
+  float* lse;
+  int32_t* dev_status;
+  void* workspace;
+};
+size_t kv_attention_ws_bytes(int T, int B, int Hq, int Hkv, int D);
+cudaError_t launch_kv_attention(const KvAttention& a, cudaStream_t st);
+cudaError_t launch_block_norm(const void* x, int64_t ld_x, const void* a, int a_dtype, int64_t ld_a, const void* gate,
+                              int64_t gate_ld_t, int64_t gate_ld_c, const void* w_post, const void* w_pre, float alpha,
+                              float eps, int T, int H, void* y, void* h, cudaStream_t st);
+
 }  // namespace nvfp4moe
