@@ -637,14 +637,12 @@ def kv_plan(ctx_lens, new_lens, block_table, free_pages, free_count, page_size, 
             _is(free_count, _I32, (1,))):
         _refuse("ctx_lens, new_lens [B], free_pages [N] and free_count [1] must be contiguous int32")
     ld, M = _table_dims(block_table, B)
-    # one allocation, each part on a 16-byte boundary
-    n0, n1, n2 = (B + 4) & -4, (B + 3) & -4, (T + 3) & -4
-    buf = _empty((n0 + n1 + n2 + 4,), _I32, ctx_lens.device)
-    start, _, kv, _, slots, _, left, _ = buf.split_with_sizes((B + 1, n0 - B - 1, B, n1 - B, T, n2 - T, 1, 3))
-    p = buf.data_ptr()
+    dev = ctx_lens.device
+    start, kv = _empty((B + 1,), _I32, dev), _empty((B,), _I32, dev)
+    slots, left = _empty((T,), _I32, dev), _empty((1,), _I32, dev)
     _check("kv_plan", L.kv_plan(_addr(ctx_lens), _addr(new_lens), B, page_size, _addr(block_table), ld, M,
-                                _addr(free_pages), N, _addr(free_count), T, p, p + 4 * n0, p + 4 * (n0 + n1),
-                                p + 4 * (n0 + n1 + n2), _opt(dev_status), _raw_stream(ctx_lens)))
+                                _addr(free_pages), N, _addr(free_count), T, start.data_ptr(), kv.data_ptr(),
+                                slots.data_ptr(), left.data_ptr(), _opt(dev_status), _raw_stream(ctx_lens)))
     return dict(query_start=start, kv_lens=kv, slot_map=slots, free_left=left)
 
 

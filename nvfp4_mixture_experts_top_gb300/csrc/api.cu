@@ -798,7 +798,7 @@ int kv_attention(const void* q, int64_t ld_q, const uint8_t* k_codes, const uint
   if ((D != 64 && D != 128) || !page_size_ok(page_size) || Hq % Hkv != 0 || B > kMaxKvRequests || M < 1 ||
       ld_table < M || num_pages > INT32_MAX / page_size)
     return NVFP4_E_SHAPE;
-  if (ld_q < (int64_t)Hq * D || ld_q % 8 != 0) return NVFP4_E_SHAPE;
+  if (ld_q < (int64_t)Hq * D || ld_q % 8 != 0 || (int64_t)T * Hq > INT32_MAX) return NVFP4_E_SHAPE;
   if (T == 0 || B == 0) return NVFP4_OK;
   if (q == nullptr || k_codes == nullptr || k_exps == nullptr || v_codes == nullptr || v_exps == nullptr ||
       block_table == nullptr || kv_lens == nullptr || query_start == nullptr || out == nullptr)

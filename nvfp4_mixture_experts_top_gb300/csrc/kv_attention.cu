@@ -1,4 +1,25 @@
-// kv_attention.cu -- attention over the paged 8-bit key/value cache.
+// kv_attention.cu -- attention over the paged 8-bit key/value cache:
+//   s_j = scale * q . k_j,   out = sum_j softmax(s)_j v_j,   lse = ln sum_j exp s_j
+// for few query rows per request and K/V head (single tokens, drafted tokens).
+//
+// Bound: every cached byte of a request is read once for all query heads of a
+// K/V head; 2 * D bytes and 4 * D * rows flops per key leave HBM as the limit
+// up to some tens of rows.  So the kernel is built to keep loads in flight:
+//  - the work is cut into units of 128 keys of one (request, K/V head, row
+//    tile), and the CTAs that fit on the GPU take equal ranges of all units,
+//    whatever the lengths.  A CTA that ends inside a sequence leaves a partial
+//    result, and a small second kernel joins them in order (no atomics: the
+//    result repeats bit for bit);
+//  - each warp streams 32-key tiles through its own ring of shared memory with
+//    cp.async, so no barrier stands between loads and arithmetic;
+//  - arithmetic is mma.sync m16n8k16 on f16 with fp32 accumulation: every E4M3
+//    value is an f16 value, and a query row is carried as f16 with its own
+//    power of two.  Keys (and the head dimension of V) are the 16-row side and
+//    query rows the 8-column side, so 8 rows cost half of what 16 do.  tcgen05
+//    would need the operands converted through shared or tensor memory for
+//    less than a tenth of its rate.
+// Softmax statistics and outputs are fp32.  Weights are rounded to f16 after a
+// shift by 2^12 (so that they keep 11 bits down to 2^-26 of the largest).
 #include "common.cuh"
 #include "kernels.h"
 #include "kv.cuh"
@@ -6,93 +27,639 @@
 namespace nvfp4moe {
 namespace {
 
-struct AttnParams {
+constexpr int kWarps = 4;
+constexpr int kThreads = kWarps * 32;
+constexpr int kTile = 32;                 // keys of a warp's step
+constexpr int kUnit = kWarps * kTile;     // keys of a work unit
+constexpr int kStages = 3;                // ring slots of a warp
+constexpr int kWholeUnits = 4;            // sequences up to this long are not split
+constexpr float kBoost = 12.0f;           // log2 of the weights' shift
+constexpr int kFarExp = -60;              // value blocks further below the largest one count as this far
+
+// The sequence -- request, K/V head, row tile -- that a CTA's range starts in,
+// for the join: units of it before the range, units of it in all, its first
+// output row (token * group + head in group), K/V head and rows.
+struct Cut {
+  int32_t before, span, row, head, rows, pad[3];
+};
+
+struct Params {
   const __nv_bfloat16* q;
   const uint8_t *k_codes, *k_exps, *v_codes, *v_exps;
   const int32_t *table, *kv_lens, *query_start;
   __nv_bfloat16* out;
   float* lse;
   int32_t* dev_status;
+  float* part;      // [CTA][2][rows][D] partial outputs
+  float* part_lse;  // [CTA][2][rows] their log2-sums
+  Cut* cut;         // [CTA]
+  int64_t* total;   // units of the whole call
   int64_t ld_q, ld_table, num_pages;
   int M, T, B, Hq, Hkv, shift;
   float scale;
 };
 
-// One warp per query token and head, one key at a time: the running maximum,
-// sum and output of a softmax in registers, D / 32 elements per lane.
+// A request as the kernel sees it: lengths cut to what the table, q and out hold.
+struct Request {
+  int q0, n, kv;
+  bool bad;
+};
+__device__ __forceinline__ Request get_request(const Params& p, int b) {
+  Request r;
+  const int a = p.query_start[b], e = p.query_start[b + 1], kv = p.kv_lens[b];
+  r.q0 = min(max(a, 0), p.T);
+  const int q1 = min(max(e, r.q0), p.T);
+  r.n = q1 - r.q0;
+  const int64_t cap = (int64_t)p.M << p.shift;
+  r.kv = kv < 0 ? 0 : (kv > cap ? (int)cap : kv);
+  r.bad = r.q0 != a || q1 != e || r.kv != kv;
+  return r;
+}
+__device__ __forceinline__ int units_of(int kv) { return kv > kUnit ? (kv + kUnit - 1) / kUnit : 1; }
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool valid) {
+  const int bytes = valid ? 16 : 0;  // 0: the destination is zero-filled
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// D += A B, A [16 x 16] f16 (row), B [16 x 8] f16 (column), fp32 accumulators.
+__device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                         uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+// Transpose of an 8 x 8 matrix of 16-bit elements held two to a lane.
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t a) {
+  uint32_t d;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
+  return d;
+}
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
+  const __half2 h = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+// Byte offset of 16-byte chunk c of key row r in a tile's [32][D] codes.  The
+// permutation makes both access patterns free of bank conflicts: keys as MMA
+// rows (lanes read rows g, chunks t and t + 4) and as MMA depth (lanes read
+// rows 2t, 2t + 1, chunk g).
 template <int D>
-__global__ void __launch_bounds__(256) kv_attention_kernel(const AttnParams p) {
-  constexpr int E = D / 32;
-  const int lane = threadIdx.x & 31;
+__device__ __forceinline__ uint32_t tile_offset(int r, int c) {
+  if (D == 128) return r * 128 + ((c ^ (r & 6) ^ ((r & 1) << 2)) << 4);
+  return (r >> 1) * 128 + (((((r & 1) << 2) | c) ^ (r & 6)) << 4);
+}
+
+template <int D, int NT>
+struct Geo {
+  static constexpr int ROWS = 8 * NT;
+  static constexpr int TILE_BYTES = kTile * D;        // codes of K or of V
+  static constexpr int STAGE_BYTES = 2 * TILE_BYTES;
+  static constexpr int WARP_BYTES = kStages * STAGE_BYTES;
+  static constexpr int RING_BYTES = kWarps * WARP_BYTES;
+  static constexpr int HEAD_BYTES = kWarps * kStages * 16;
+  static constexpr int SMEM_BYTES = RING_BYTES + HEAD_BYTES;
+  static constexpr int CTAS = D == 128 ? 2 : 4;       // of an SM: about 128 KB of loads in flight
+  static_assert(ROWS * D * 4 <= WARP_BYTES, "the warps' outputs are joined in the ring");
+};
+
+// Where a CTA's range begins.
+struct Start {
+  int b;
+  int64_t off;
+};
+
+template <int D, int NT>
+__global__ void __launch_bounds__(kThreads, (Geo<D, NT>::CTAS)) kv_attention_kernel(const Params p) {
+  using G = Geo<D, NT>;
+  constexpr int ROWS = G::ROWS;
+  constexpr int NQ = D / 16;   // MMA steps over the head dimension
+  constexpr int NV = D / 16;   // 16-row blocks of V^T
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ int64_t s_sum[2][kWarps];
+  __shared__ int s_long[kWarps];
+  __shared__ Start s_start;
+  __shared__ float s_m[kWarps][ROWS], s_l[kWarps][ROWS];
+  __shared__ int s_u[kWarps];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
+  const int group = p.Hq / p.Hkv;
   pdl_wait();
   pdl_trigger();
-  const int64_t item = ((int64_t)blockIdx.x * 256 + threadIdx.x) >> 5;
-  const int t = (int)(item / p.Hq), h = (int)(item % p.Hq);
-  if (t >= p.T || t < p.query_start[0] || t >= p.query_start[p.B]) return;
-  if (lane == 0 && (p.query_start[0] < 0 || p.query_start[p.B] > p.T)) report_status(p.dev_status, NVFP4_E_BAD_PAGE);
-  int lo = 0, hi = p.B;
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (p.query_start[mid] <= t) lo = mid;
-    else hi = mid;
+
+  // ---- the CTA's range of the work: units if some sequence is longer than
+  // kWholeUnits, else whole sequences (nothing to join then)
+  const int per = (p.B + kThreads - 1) / kThreads;
+  const int b0 = min(tid * per, p.B), b1 = min(b0 + per, p.B);
+  int64_t seqs = 0, units = 0;
+  int longest = 0;
+  for (int b = b0; b < b1; ++b) {
+    const Request r = get_request(p, b);
+    const int tiles = (int)(((int64_t)r.n * group + ROWS - 1) / ROWS), ku = units_of(r.kv);
+    seqs += (int64_t)tiles * p.Hkv;
+    units += (int64_t)tiles * p.Hkv * ku;
+    if (tiles) longest = max(longest, ku);
+    if (blockIdx.x == 0 && r.bad) report_status(p.dev_status, NVFP4_E_BAD_PAGE);
   }
-  const int S = 1 << p.shift;
-  int64_t kv = p.kv_lens[lo];
-  if (kv < 0 || kv > (int64_t)p.M * S) {
-    if (lane == 0) report_status(p.dev_status, NVFP4_E_BAD_PAGE);
-    kv = kv < 0 ? 0 : (int64_t)p.M * S;
-  }
-  const int64_t keys = kv - p.query_start[lo + 1] + t + 1;
-  const int head = h / (p.Hq / p.Hkv);
-  float q[E], o[E];
+  int64_t in_s = seqs, in_u = units;
 #pragma unroll
-  for (int i = 0; i < E; ++i) {
-    q[i] = __bfloat162float(p.q[t * p.ld_q + h * D + lane * E + i]) * p.scale;
-    o[i] = 0.0f;
+  for (int d = 1; d < 32; d <<= 1) {
+    const int64_t a = __shfl_up_sync(0xFFFFFFFFu, in_s, d), c = __shfl_up_sync(0xFFFFFFFFu, in_u, d);
+    if (lane >= d) {
+      in_s += a;
+      in_u += c;
+    }
+    longest = max(longest, __shfl_xor_sync(0xFFFFFFFFu, longest, d));
   }
-  float m = -INFINITY, l = 0.0f;
-  for (int64_t j = 0; j < keys; ++j) {
-    const int page = p.table[lo * p.ld_table + (j >> p.shift)];
-    if (page < 0 || page >= p.num_pages) {
-      if (lane == 0) report_status(p.dev_status, NVFP4_E_BAD_PAGE);
+  if (lane == 31) {
+    s_sum[0][warp] = in_s;
+    s_sum[1][warp] = in_u;
+    s_long[warp] = longest;
+  }
+  __syncthreads();
+  longest = max(max(s_long[0], s_long[1]), max(s_long[2], s_long[3]));
+  const bool split = longest > kWholeUnits;
+  int64_t total = 0, before = split ? in_u - units : in_s - seqs;
+  for (int w = 0; w < kWarps; ++w) {
+    const int64_t x = s_sum[split ? 1 : 0][w];
+    total += x;
+    if (w < warp) before += x;
+  }
+  const int64_t lo = total * blockIdx.x / gridDim.x, hi = total * (blockIdx.x + 1) / gridDim.x;
+  if (lo < hi && before <= lo && lo < before + (split ? units : seqs)) {
+    for (int b = b0; b < b1; ++b) {
+      const Request r = get_request(p, b);
+      const int64_t w = ((int64_t)r.n * group + ROWS - 1) / ROWS * p.Hkv * (split ? units_of(r.kv) : 1);
+      if (lo < before + w) {
+        s_start.b = b;
+        s_start.off = lo - before;
+        break;
+      }
+      before += w;
+    }
+  }
+  __syncthreads();
+  if (blockIdx.x == 0 && tid == 0) *p.total = total;
+  if (lo >= hi) {
+    if (tid == 0) p.cut[blockIdx.x].before = 0;
+    return;
+  }
+  int b = s_start.b;
+  int64_t off = s_start.off, pos = lo;
+
+  uint8_t* ring = smem + warp * G::WARP_BYTES;
+  const uint32_t ring_u = smem_u32(ring);
+  uint2* head = reinterpret_cast<uint2*>(smem + G::RING_BYTES) + warp * kStages * 2;
+  const int S = 1 << p.shift;
+  bool first = true;
+
+  while (pos < hi && b < p.B) {
+    const Request rq = get_request(p, b);
+    const int rows = rq.n * group, tiles = (rows + ROWS - 1) / ROWS, ku = units_of(rq.kv), span = split ? ku : 1;
+    if (off >= (int64_t)tiles * p.Hkv * span) {
+      ++b;
+      off = 0;
       continue;
     }
-    const int64_t block = (int64_t)page * p.Hkv + head;
-    const int64_t at = (block * S + (j & (S - 1))) * D + lane * E;
-    const float ks = exp2_int(p.k_exps[block] - 127), vs = exp2_int(p.v_exps[block] - 127);
-    float s = 0.0f;
+    const int seq = (int)(off / span), u0 = (int)(off % span);
+    const int take = (int)min((int64_t)(span - u0), hi - pos);
+    const int hk = seq / tiles, row0 = (seq % tiles) * ROWS;
+    const int nrows = min(ROWS, rows - row0);
+    if (first && tid == 0) {
+      p.cut[blockIdx.x] = {split ? u0 : 0, span, rq.q0 * group + row0, hk, nrows, {0, 0, 0}};
+    }
+    // keys that the last row of the tile sees
+    const int limit = min(rq.kv, rq.kv - rq.n + (row0 + nrows - 1) / group + 1);
+    const int t0 = split ? u0 * kWarps : 0;
+    const int t1 = min(split ? (u0 + take) * kWarps : INT32_MAX, limit > 0 ? (limit + kTile - 1) / kTile : 0);
+    const int nt = t1 - t0 - warp > 0 ? (t1 - t0 - warp + kWarps - 1) / kWarps : 0;  // this warp's tiles
+
+    // pages of 32 of the warp's tiles at a time, one (or two, of 16 keys) per
+    // lane: ids, -1 where there is none, and the exponent bytes
+    int page_a = -1, page_b = -1;
+    uint32_t exps = 0;
+    auto load_pages = [&](int j) {
+      page_a = page_b = -1;
+      exps = 0;
+      if (j + lane < nt) {
+        const int key = (t0 + warp + (j + lane) * kWarps) * kTile;
+        const int64_t row = b * p.ld_table;
+        page_a = p.table[row + (key >> p.shift)];
+        page_b = p.shift == 4 && key + 16 < limit ? p.table[row + (key >> p.shift) + 1] : page_a;
+        if (page_a < 0 || page_a >= p.num_pages) {
+          page_a = -1;
+          report_status(p.dev_status, NVFP4_E_BAD_PAGE);
+        }
+        if (page_b < 0 || page_b >= p.num_pages) {
+          page_b = -1;
+          report_status(p.dev_status, NVFP4_E_BAD_PAGE);
+        }
+        if (page_a >= 0) {
+          const int64_t at = (int64_t)page_a * p.Hkv + hk;
+          exps = p.k_exps[at] | (uint32_t)p.v_exps[at] << 8;
+        }
+        if (page_b >= 0) {
+          const int64_t at = (int64_t)page_b * p.Hkv + hk;
+          exps |= (uint32_t)p.k_exps[at] << 16 | (uint32_t)p.v_exps[at] << 24;
+        }
+      }
+    };
+    // copies of tile j into ring slot s
+    auto issue = [&](int j, int s) {
+      if (j < nt) {
+        if ((j & 31) == 0) load_pages(j);
+        const int pa = __shfl_sync(0xFFFFFFFFu, page_a, j & 31), pb = __shfl_sync(0xFFFFFFFFu, page_b, j & 31);
+        const uint32_t ex = __shfl_sync(0xFFFFFFFFu, exps, j & 31);
+        if (lane == 0) head[s * 2] = make_uint2(ex, (pa < 0 ? 1u : 0u) | (pb < 0 ? 2u : 0u));
+        const int key0 = (t0 + warp + j * kWarps) * kTile;
+        constexpr int CPR = D / 16;          // 16-byte chunks of a row
+        constexpr int RPI = 32 / CPR;        // rows of a warp's copy
+        const int64_t ba = ((int64_t)max(pa, 0) * p.Hkv + hk) << p.shift;
+        const int64_t bb = ((int64_t)max(pb, 0) * p.Hkv + hk) << p.shift;
+        const uint32_t base = ring_u + s * G::STAGE_BYTES;
 #pragma unroll
-    for (int i = 0; i < E; ++i) s += q[i] * (f32_from_e4m3(p.k_codes[at + i]) * ks);
+        for (int i = 0; i < kTile / RPI; ++i) {
+          const int r = i * RPI + lane / CPR, c = lane % CPR, key = key0 + r;
+          const bool second = r >= 16;
+          const bool valid = key < limit && (second ? pb : pa) >= 0;
+          const int64_t at = ((second ? bb : ba) + (key & (S - 1))) * D + c * 16;
+          const uint32_t dst = base + tile_offset<D>(r, c);
+          cp_async16(dst, p.k_codes + at, valid);
+          cp_async16(dst + G::TILE_BYTES, p.v_codes + at, valid);
+        }
+      }
+      cp_async_commit();
+    };
 #pragma unroll
-    for (int d = 16; d > 0; d >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, d);
-    const float m1 = fmaxf(m, s);
-    if (m1 == -INFINITY && s == -INFINITY) continue;  // (a NaN goes on)
-    const float f = expf(m - m1), w = expf(s - m1);
-    m = m1;
-    l = l * f + w;
+    for (int s = 0; s < kStages - 1; ++s) issue(s, s);
+
+    // ---- query rows: lane (g, t) holds row g's elements for its keys' chunks,
+    // as f16 times the row's power of two
+    uint32_t qf[NT][NQ][2];
+    float qs[NT][2];     // log2 logit per accumulator unit, rows 2t and 2t + 1
+    int lim[NT][2];      // keys that the row sees
 #pragma unroll
-    for (int i = 0; i < E; ++i) o[i] = o[i] * f + w * (f32_from_e4m3(p.v_codes[at + i]) * vs);
+    for (int n = 0; n < NT; ++n) {
+      const int r = row0 + n * 8 + g;
+      float v[D / 4], amax = 0.0f;
+      const __nv_bfloat16* src =
+          p.q + (int64_t)(rq.q0 + r / group) * p.ld_q + (int64_t)(hk * group + r % group) * D + 16 * t;
+#pragma unroll
+      for (int h = 0; h < D / 64; ++h) {
+        uint4 w[2] = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
+        if (r < rows) {
+          w[0] = *reinterpret_cast<const uint4*>(src + 64 * h);
+          w[1] = *reinterpret_cast<const uint4*>(src + 64 * h + 8);
+        }
+        const uint32_t x[8] = {w[0].x, w[0].y, w[0].z, w[0].w, w[1].x, w[1].y, w[1].z, w[1].w};
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          v[h * 16 + 2 * i] = __uint_as_float(x[i] << 16);
+          v[h * 16 + 2 * i + 1] = __uint_as_float(x[i] & 0xFFFF0000u);
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < D / 4; ++i) amax = fmaxf(amax, fabsf(v[i]));
+      amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 1));
+      amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 2));
+      const int e = amax == 0.0f ? 0 : min(14 - floor_log2(amax), 126);
+      const float f = exp2_int(e);
+#pragma unroll
+      for (int k = 0; k < NQ; ++k) {
+        qf[n][k][0] = pack_f16(v[4 * k] * f, v[4 * k + 1] * f);
+        qf[n][k][1] = pack_f16(v[4 * k + 2] * f, v[4 * k + 3] * f);
+      }
+      const float rs = p.scale * 1.4426950408889634f * exp2_int(-e);
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        qs[n][c] = __shfl_sync(0xFFFFFFFFu, rs, (2 * t + c) * 4);
+        const int rr = row0 + n * 8 + 2 * t + c;
+        lim[n][c] = rr < rows ? min(rq.kv, rq.kv - rq.n + rr / group + 1) : 0;
+      }
+    }
+    const int all_see = rq.kv - rq.n + row0 / group + 1;  // keys below this are seen by every row
+
+    float o[NT][NV][4], m[NT][2], l[NT][2];
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+#pragma unroll
+      for (int i = 0; i < NV; ++i) o[n][i][0] = o[n][i][1] = o[n][i][2] = o[n][i][3] = 0.0f;
+      m[n][0] = m[n][1] = -INFINITY;
+      l[n][0] = l[n][1] = 0.0f;
+    }
+    int unit_exp = -127;  // outputs are held in units of 2^unit_exp, the largest value exponent so far
+
+    int slot = 0;
+    for (int j = 0; j < nt; ++j) {
+      cp_async_wait<kStages - 2>();
+      __syncwarp();
+      issue(j + kStages - 1, slot == 0 ? kStages - 1 : slot - 1);
+      const uint2 hd = head[slot * 2];
+      const uint8_t* kt = ring + slot * G::STAGE_BYTES;
+      const uint8_t* vt = kt + G::TILE_BYTES;
+      const int key0 = (t0 + warp + j * kWarps) * kTile;
+
+      // S^T = K Q^T, two blocks of 16 keys
+      float s[NT][2][4];
+#pragma unroll
+      for (int kb = 0; kb < 2; ++kb) {
+#pragma unroll
+        for (int n = 0; n < NT; ++n) s[n][kb][0] = s[n][kb][1] = s[n][kb][2] = s[n][kb][3] = 0.0f;
+#pragma unroll
+        for (int h = 0; h < D / 64; ++h) {
+          const uint4 ka = *reinterpret_cast<const uint4*>(kt + tile_offset<D>(kb * 16 + g, h * 4 + t));
+          const uint4 kc = *reinterpret_cast<const uint4*>(kt + tile_offset<D>(kb * 16 + g + 8, h * 4 + t));
+          const uint32_t wa[4] = {ka.x, ka.y, ka.z, ka.w}, wc[4] = {kc.x, kc.y, kc.z, kc.w};
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const uint32_t a0 = kv::decode2((uint16_t)wa[i]), a2 = kv::decode2((uint16_t)(wa[i] >> 16));
+            const uint32_t a1 = kv::decode2((uint16_t)wc[i]), a3 = kv::decode2((uint16_t)(wc[i] >> 16));
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+              mma16816(s[n][kb], a0, a1, a2, a3, qf[n][h * 4 + i][0], qf[n][h * 4 + i][1]);
+          }
+        }
+      }
+      // logits in log2 units; keys that a row does not see are -inf
+      const float ks[2] = {exp2_int((int)(hd.x & 255) - 127), exp2_int((int)(hd.x >> 16 & 255) - 127)};
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int kb = 0; kb < 2; ++kb)
+#pragma unroll
+          for (int c = 0; c < 4; ++c) s[n][kb][c] = s[n][kb][c] * qs[n][c & 1] * ks[kb];
+      if (key0 + kTile > all_see || hd.y) {
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int kb = 0; kb < 2; ++kb)
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+              if (key0 + kb * 16 + g + (c >> 1) * 8 >= lim[n][c & 1] || (hd.y >> kb & 1)) s[n][kb][c] = -INFINITY;
+      }
+      // value exponents of the two blocks relative to the largest so far
+      const int va = hd.y & 1 ? -127 : (int)(hd.x >> 8 & 255) - 127, vb = hd.y & 2 ? -127 : (int)(hd.x >> 24) - 127;
+      const int ue = max(unit_exp, max(va, vb));
+      const float vs[2] = {exp2_int(max(va - ue, kFarExp)), exp2_int(max(vb - ue, kFarExp))};
+      const float us = exp2_int(max(unit_exp - ue, -127));
+      unit_exp = ue;
+      uint32_t pf[NT][2][2];  // weights as the MMA's 16 x 8 operand
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        float f[2];
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          float mx = fmaxf(fmaxf(s[n][0][c], s[n][0][c + 2]), fmaxf(s[n][1][c], s[n][1][c + 2]));
+          mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 4));
+          mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 8));
+          mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 16));
+          const float m1 = fmaxf(m[n][c], mx), ms = m1 == -INFINITY ? 0.0f : m1;
+          f[c] = ex2(m[n][c] - ms);
+          m[n][c] = m1;
+          float sum = 0.0f;
+#pragma unroll
+          for (int kb = 0; kb < 2; ++kb)
+#pragma unroll
+            for (int d = 0; d < 4; d += 2) {
+              const float w = ex2(s[n][kb][c + d] - ms + kBoost);
+              sum += w;
+              s[n][kb][c + d] = w * vs[kb];
+            }
+          l[n][c] = l[n][c] * f[c] + sum;
+          f[c] *= us;
+        }
+#pragma unroll
+        for (int kb = 0; kb < 2; ++kb) {
+          pf[n][kb][0] = transpose8x8(pack_f16(s[n][kb][0], s[n][kb][1]));
+          pf[n][kb][1] = transpose8x8(pack_f16(s[n][kb][2], s[n][kb][3]));
+        }
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+          o[n][i][0] *= f[0];
+          o[n][i][1] *= f[1];
+          o[n][i][2] *= f[0];
+          o[n][i][3] *= f[1];
+        }
+      }
+      // O^T += V^T P^T: lane (g, t) reads D / 8 elements of keys 2t, 2t+1, 2t+8, 2t+9
+#pragma unroll
+      for (int kb = 0; kb < 2; ++kb) {
+        constexpr int NW = D / 32;  // 4-byte words of a lane's elements of a key
+        uint32_t w[4][NW];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int r = kb * 16 + 2 * t + (i & 1) + (i >> 1) * 8;
+          if constexpr (D == 128) {
+            const uint4 x = *reinterpret_cast<const uint4*>(vt + tile_offset<D>(r, g));
+            w[i][0] = x.x, w[i][1] = x.y, w[i][2] = x.z, w[i][3] = x.w;
+          } else {
+            const uint2 x = *reinterpret_cast<const uint2*>(vt + tile_offset<D>(r, g >> 1) + (g & 1) * 8);
+            w[i][0] = x.x, w[i][1] = x.y;
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < NW; ++i)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            // elements 2h, 2h + 1 of word i: (key 2t, key 2t + 1) pairs of each
+            const uint32_t x = __byte_perm(w[0][i], w[1][i], h ? 0x7362 : 0x5140);
+            const uint32_t y = __byte_perm(w[2][i], w[3][i], h ? 0x7362 : 0x5140);
+            const uint32_t a0 = kv::decode2((uint16_t)x), a1 = kv::decode2((uint16_t)(x >> 16));
+            const uint32_t a2 = kv::decode2((uint16_t)y), a3 = kv::decode2((uint16_t)(y >> 16));
+#pragma unroll
+            for (int n = 0; n < NT; ++n) mma16816(o[n][2 * i + h], a0, a1, a2, a3, pf[n][kb][0], pf[n][kb][1]);
+          }
+      }
+      slot = slot + 1 == kStages ? 0 : slot + 1;
+    }
+    cp_async_wait<0>();
+    __syncwarp();
+
+    // ---- join the four warps: lane (g, t) holds D / 8 consecutive elements,
+    // from g * D / 8, of rows 2t and 2t + 1
+    float* ow = reinterpret_cast<float*>(ring);
+    constexpr int EL = D / 8;
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        float sum = l[n][c];
+        sum += __shfl_xor_sync(0xFFFFFFFFu, sum, 4);
+        sum += __shfl_xor_sync(0xFFFFFFFFu, sum, 8);
+        sum += __shfl_xor_sync(0xFFFFFFFFu, sum, 16);
+        const int r = n * 8 + 2 * t + c;
+        if (g == 0) {
+          s_m[warp][r] = m[n][c];
+          s_l[warp][r] = sum;
+        }
+#pragma unroll
+        for (int i = 0; i < EL / 4; ++i)
+          *reinterpret_cast<float4*>(ow + r * D + g * EL + 4 * i) =
+              make_float4(o[n][2 * i][c], o[n][2 * i][c + 2], o[n][2 * i + 1][c], o[n][2 * i + 1][c + 2]);
+      }
+    if (lane == 0) s_u[warp] = unit_exp;
+    __syncthreads();
+    const bool whole = take == span;
+    const int64_t part = (int64_t)blockIdx.x * 2 + (first ? 0 : 1);
+    const int umax = max(max(s_u[0], s_u[1]), max(s_u[2], s_u[3]));
+    constexpr int TPR = D / 4;  // threads of a row, four elements each
+    for (int r = tid / TPR; r < nrows; r += kThreads / TPR) {
+      const int d = tid % TPR * 4;
+      float mx = -INFINITY;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) mx = fmaxf(mx, s_m[w][r]);
+      const float ms = mx == -INFINITY ? 0.0f : mx;
+      float sum = 0.0f;
+      float4 acc = make_float4(0, 0, 0, 0);
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) {
+        const float f = ex2(s_m[w][r] - ms), fu = f * exp2_int(max(s_u[w] - umax, -127));
+        sum += s_l[w][r] * f;
+        const float4 x = *reinterpret_cast<const float4*>(smem + w * G::WARP_BYTES + (r * D + d) * 4);
+        acc.x += x.x * fu, acc.y += x.y * fu, acc.z += x.z * fu, acc.w += x.w * fu;
+      }
+      const bool none = sum == 0.0f;
+      const float inv = none ? 0.0f : 1.0f / sum, us = exp2_int(umax);
+      acc = none ? make_float4(0, 0, 0, 0)
+                 : make_float4(acc.x * inv * us, acc.y * inv * us, acc.z * inv * us, acc.w * inv * us);
+      const float lse2 = none ? -INFINITY : mx + (log2f(sum) - kBoost);
+      if (whole) {
+        const int rr = row0 + r;
+        const int64_t at = (int64_t)(rq.q0 + rr / group) * p.Hq + hk * group + rr % group;
+        const __nv_bfloat162 lo2 = __floats2bfloat162_rn(acc.x, acc.y), hi2 = __floats2bfloat162_rn(acc.z, acc.w);
+        *reinterpret_cast<uint2*>(p.out + at * D + d) =
+            make_uint2(*reinterpret_cast<const uint32_t*>(&lo2), *reinterpret_cast<const uint32_t*>(&hi2));
+        if (p.lse != nullptr && d == 0) p.lse[at] = lse2 * 0.6931471805599453f;
+      } else {
+        *reinterpret_cast<float4*>(p.part + (part * ROWS + r) * D + d) = acc;
+        if (d == 0) p.part_lse[part * ROWS + r] = lse2;
+      }
+    }
+    __syncthreads();  // the ring is free again
+    first = false;
+    pos += take;
+    off += take;
+  }
+}
+
+// Joins the partial results of a sequence, a warp per row, parts in order.  CTA
+// c = blockIdx.x + 1 takes the sequence that its range starts in, if no earlier
+// range starts inside it.
+template <int D, int NT>
+__global__ void __launch_bounds__(128) kv_attention_join_kernel(const Params p, int ctas) {
+  constexpr int ROWS = Geo<D, NT>::ROWS;
+  constexpr int E = D / 32;
+  pdl_wait();
+  pdl_trigger();
+  const int c = blockIdx.x + 1, lane = threadIdx.x & 31, r = blockIdx.y * 4 + (threadIdx.x >> 5);
+  const Cut cut = p.cut[c];
+  if (cut.before == 0 || r >= cut.rows) return;
+  const int64_t W = *p.total;
+  // unit u belongs to the last CTA whose range starts at or before it
+  auto owner = [&](int64_t u) { return (int)(((u + 1) * ctas - 1) / W); };
+  const int64_t a = W * c / ctas - cut.before, e = a + cut.span;
+  const int c0 = owner(a);
+  if (owner(a + cut.before - 1) != c0) return;
+  // a part per CTA; with fewer units than CTAs, a part per unit
+  const int n = W >= ctas ? owner(e - 1) - c0 + 1 : cut.span;
+  auto row_of = [&](int k) {
+    const int64_t cta = W >= ctas ? c0 + k : owner(a + k);
+    return (cta * 2 + (W * cta / ctas >= a ? 0 : 1)) * ROWS + r;
+  };
+  float top = -INFINITY;
+  for (int k = lane; k < n; k += 32) top = fmaxf(top, p.part_lse[row_of(k)]);
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, d));
+  const float ms = top == -INFINITY ? 0.0f : top;
+  float sum = 0.0f, acc[E] = {};
+  for (int k0 = 0; k0 < n; k0 += 32) {
+    const int64_t row = row_of(min(k0 + lane, n - 1));
+    const float w = k0 + lane < n ? ex2(p.part_lse[row] - ms) : 0.0f;
+    sum += w;
+    const int m = min(32, n - k0);
+#pragma unroll 8
+    for (int k = 0; k < m; ++k) {
+      const float wk = __shfl_sync(0xFFFFFFFFu, w, k);
+      const float* src = p.part + __shfl_sync(0xFFFFFFFFu, row, k) * D + lane * E;
+#pragma unroll
+      for (int i = 0; i < E; ++i) acc[i] += wk * src[i];
+    }
   }
 #pragma unroll
-  for (int i = 0; i < E; ++i)
-    p.out[((int64_t)t * p.Hq + h) * D + lane * E + i] = __float2bfloat16(l == 0.0f ? 0.0f : o[i] / l);
-  if (p.lse != nullptr && lane == 0) p.lse[(int64_t)t * p.Hq + h] = l == 0.0f ? -INFINITY : m + logf(l);
+  for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, d);
+  const bool none = sum == 0.0f;
+  const float inv = none ? 0.0f : 1.0f / sum;
+  const int group = p.Hq / p.Hkv, rr = cut.row + r;
+  const int64_t at = (int64_t)(rr / group) * p.Hq + cut.head * group + rr % group;
+#pragma unroll
+  for (int i = 0; i < E; ++i) p.out[at * D + lane * E + i] = __float2bfloat16(none ? 0.0f : acc[i] * inv);
+  if (p.lse != nullptr && lane == 0) p.lse[at] = none ? -INFINITY : (top + log2f(sum)) * 0.6931471805599453f;
+}
+
+template <int D, int NT>
+size_t carve(Params* p, void* base) {
+  using G = Geo<D, NT>;
+  const size_t ctas = (size_t)num_sms() * G::CTAS;
+  uint8_t* b = static_cast<uint8_t*>(base);
+  size_t off = 0;
+  auto take = [&](size_t bytes) {
+    uint8_t* at = b ? b + off : nullptr;
+    off += (bytes + 255) & ~(size_t)255;
+    return at;
+  };
+  uint8_t* total = take(sizeof(int64_t));
+  uint8_t* cut = take(ctas * sizeof(Cut));
+  uint8_t* lse = take(ctas * 2 * G::ROWS * sizeof(float));
+  uint8_t* part = take(ctas * 2 * G::ROWS * D * sizeof(float));
+  if (p != nullptr) {
+    p->total = reinterpret_cast<int64_t*>(total);
+    p->cut = reinterpret_cast<Cut*>(cut);
+    p->part_lse = reinterpret_cast<float*>(lse);
+    p->part = reinterpret_cast<float*>(part);
+  }
+  return off;
+}
+
+template <int D, int NT>
+cudaError_t launch(const KvAttention& a, cudaStream_t st) {
+  using G = Geo<D, NT>;
+  Params p = {static_cast<const __nv_bfloat16*>(a.q), a.k_codes, a.k_exps, a.v_codes, a.v_exps, a.table, a.kv_lens,
+              a.query_start, static_cast<__nv_bfloat16*>(a.out), a.lse, a.dev_status, nullptr, nullptr, nullptr,
+              nullptr, a.ld_q, a.ld_table, a.num_pages, a.M, a.T, a.B, a.Hq, a.Hkv, kv::log2_page(a.page_size),
+              a.scale};
+  carve<D, NT>(&p, a.workspace);
+  cudaError_t e = ensure_dynamic_smem(reinterpret_cast<const void*>(kv_attention_kernel<D, NT>), G::SMEM_BYTES);
+  if (e != cudaSuccess) return e;
+  const int ctas = num_sms() * G::CTAS;
+  e = launch_pdl(kv_attention_kernel<D, NT>, ctas, kThreads, G::SMEM_BYTES, st, p);
+  // a table that holds no sequence long enough to be split needs no join
+  if (e != cudaSuccess || (int64_t)a.M * a.page_size <= kWholeUnits * kUnit) return e;
+  return launch_pdl(kv_attention_join_kernel<D, NT>, dim3(ctas - 1, G::ROWS / 4), 128, 0, st, p, ctas);
 }
 
 }  // namespace
 
 size_t kv_attention_ws_bytes(int T, int B, int Hq, int Hkv, int D) {
-  (void)T, (void)B, (void)Hq, (void)Hkv, (void)D;
-  return 256;
+  (void)T, (void)B, (void)Hq, (void)Hkv;
+  return D == 128 ? carve<128, 2>(nullptr, nullptr) : carve<64, 2>(nullptr, nullptr);
 }
 
+// Eight query rows per K/V head and request, or tiles of sixteen.
 cudaError_t launch_kv_attention(const KvAttention& a, cudaStream_t st) {
-  AttnParams p = {static_cast<const __nv_bfloat16*>(a.q), a.k_codes, a.k_exps, a.v_codes, a.v_exps, a.table,
-                  a.kv_lens, a.query_start, static_cast<__nv_bfloat16*>(a.out), a.lse, a.dev_status, a.ld_q,
-                  a.ld_table, a.num_pages, a.M, a.T, a.B, a.Hq, a.Hkv, kv::log2_page(a.page_size), a.scale};
-  const unsigned grid = (unsigned)(((int64_t)a.T * a.Hq * 32 + 255) / 256);
-  return a.D == 128 ? launch_pdl(kv_attention_kernel<128>, grid, 256, 0, st, p)
-                    : launch_pdl(kv_attention_kernel<64>, grid, 256, 0, st, p);
+  const bool few = (int64_t)a.max_query_len * (a.Hq / a.Hkv) <= 8;
+  if (a.D == 128) return few ? launch<128, 1>(a, st) : launch<128, 2>(a, st);
+  return few ? launch<64, 1>(a, st) : launch<64, 2>(a, st);
 }
 
 }  // namespace nvfp4moe
