@@ -10,8 +10,10 @@
 //    whatever the lengths.  A CTA that ends inside a sequence leaves a partial
 //    result, and a small second kernel joins them in order (no atomics: the
 //    result repeats bit for bit);
-//  - each warp streams 32-key tiles through its own ring of shared memory with
-//    cp.async, so no barrier stands between loads and arithmetic;
+//  - one warp of a CTA does nothing but page lookups and copies: it fills a
+//    ring of 32-key tiles (cp.async, an mbarrier per slot) and runs ahead of the
+//    arithmetic across the ends of sequences; the other warps take tiles in
+//    turn, each with its own running maximum, sum and output;
 //  - arithmetic is mma.sync m16n8k16 on f16 with fp32 accumulation: every E4M3
 //    value is an f16 value, and a query row is carried as f16 with its own
 //    power of two.  Keys (and the head dimension of V) are the 16-row side and
@@ -27,12 +29,8 @@
 namespace nvfp4moe {
 namespace {
 
-constexpr int kWarps = 4;
-constexpr int kThreads = kWarps * 32;
 constexpr int kTile = 32;                 // keys of a warp's step
-constexpr int kUnit = kWarps * kTile;     // keys of a work unit
-constexpr int kStages = 3;                // ring slots of a warp
-constexpr int kWholeUnits = 4;            // sequences up to this long are not split
+constexpr int kWholeKeys = 512;           // sequences up to this long are not split
 constexpr float kBoost = 12.0f;           // log2 of the weights' shift
 constexpr int kFarExp = -60;              // value blocks further below the largest one count as this far
 
@@ -75,8 +73,6 @@ __device__ __forceinline__ Request get_request(const Params& p, int b) {
   r.bad = r.q0 != a || q1 != e || r.kv != kv;
   return r;
 }
-__device__ __forceinline__ int units_of(int kv) { return kv > kUnit ? (kv + kUnit - 1) / kUnit : 1; }
-
 __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -87,11 +83,11 @@ __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool v
   const int bytes = valid ? 16 : 0;  // 0: the destination is zero-filled
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
 }
-__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void cp_async_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+// Arrive on `bar` (once per calling thread) when this thread's copies so far have landed.
+__device__ __forceinline__ void cp_async_arrive(uint64_t* bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
+__device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 
 // D += A B, A [16 x 16] f16 (row), B [16 x 8] f16 (column), fp32 accumulators.
 __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
@@ -125,200 +121,253 @@ __device__ __forceinline__ uint32_t tile_offset(int r, int c) {
 template <int D, int NT>
 struct Geo {
   static constexpr int ROWS = 8 * NT;
-  static constexpr int TILE_BYTES = kTile * D;        // codes of K or of V
-  static constexpr int STAGE_BYTES = 2 * TILE_BYTES;
-  static constexpr int WARP_BYTES = kStages * STAGE_BYTES;
-  static constexpr int RING_BYTES = kWarps * WARP_BYTES;
-  static constexpr int HEAD_BYTES = kWarps * kStages * 16;
-  static constexpr int SMEM_BYTES = RING_BYTES + HEAD_BYTES;
-  static constexpr int CTAS = D == 128 ? 2 : 4;       // of an SM: about 128 KB of loads in flight
-  static_assert(ROWS * D * 4 <= WARP_BYTES, "the warps' outputs are joined in the ring");
+  // warps that compute: with the copying one, two CTAs give each of an SM's
+  // four schedulers four warps of 128 registers (three of 168)
+  static constexpr int WARPS = D * NT > 128 ? 5 : 7;
+  static constexpr int THREADS = (WARPS + 1) * 32;
+  static constexpr int CTAS = 2;                       // of an SM
+  static constexpr int UNIT = WARPS * kTile;           // keys of a work unit
+  static constexpr int TILE_BYTES = kTile * D;         // codes of K or of V
+  static constexpr int SLOT_BYTES = 2 * TILE_BYTES;
+  static constexpr int JOIN_BYTES = WARPS * ROWS * D * 4;
+  static constexpr int SLOTS = (111 * 1024 + D * 8 - JOIN_BYTES) / SLOT_BYTES;
+  static constexpr int RING_BYTES = SLOTS * SLOT_BYTES;
+  static constexpr int SMEM_BYTES = RING_BYTES + JOIN_BYTES;
+  static_assert(WARPS < SLOTS, "a warp's next tile is at most one lap ahead");
 };
 
-// Where a CTA's range begins.
-struct Start {
-  int b;
-  int64_t off;
+// The pieces of sequences that a CTA's range of the work consists of, in order.
+template <int D, int NT>
+struct Pieces {
+  int b;          // request
+  int64_t off;    // of the range in the request's work
+  int64_t pos, hi;
+  bool split;
+  // the current piece
+  Request rq;
+  int hk, row0, rows, nrows, span, u0, take;
+  int limit;      // keys that the last row of the tile sees
+  int t0, t1;     // its tiles
+
+  __device__ __forceinline__ static int units(int kv) {
+    return kv > Geo<D, NT>::UNIT ? (kv + Geo<D, NT>::UNIT - 1) / Geo<D, NT>::UNIT : 1;
+  }
+  __device__ __forceinline__ static int64_t row_tiles(int n, int group) {
+    return ((int64_t)n * group + Geo<D, NT>::ROWS - 1) / Geo<D, NT>::ROWS;
+  }
+  __device__ __forceinline__ bool next(const Params& p, int group) {
+    while (pos < hi && b < p.B) {
+      rq = get_request(p, b);
+      const int tiles = (int)row_tiles(rq.n, group);
+      span = split ? units(rq.kv) : 1;
+      if (off >= (int64_t)tiles * p.Hkv * span) {
+        ++b;
+        off = 0;
+        continue;
+      }
+      const int seq = (int)(off / span);
+      u0 = (int)(off - (int64_t)seq * span);
+      take = (int)min((int64_t)(span - u0), hi - pos);
+      hk = seq / tiles;
+      row0 = (seq - hk * tiles) * Geo<D, NT>::ROWS;
+      rows = rq.n * group;
+      nrows = min(Geo<D, NT>::ROWS, rows - row0);
+      limit = min(rq.kv, rq.kv - rq.n + (row0 + nrows - 1) / group + 1);
+      const int end = limit > 0 ? (limit + kTile - 1) / kTile : 0;
+      t0 = split ? u0 * Geo<D, NT>::WARPS : 0;
+      t1 = split ? min((u0 + take) * Geo<D, NT>::WARPS, end) : end;
+      pos += take;
+      off += take;
+      return true;
+    }
+    return false;
+  }
 };
 
 template <int D, int NT>
-__global__ void __launch_bounds__(kThreads, (Geo<D, NT>::CTAS)) kv_attention_kernel(const Params p) {
+__global__ void __launch_bounds__((Geo<D, NT>::THREADS), (Geo<D, NT>::CTAS)) kv_attention_kernel(const Params p) {
   using G = Geo<D, NT>;
-  constexpr int ROWS = G::ROWS;
+  using P = Pieces<D, NT>;
+  constexpr int ROWS = G::ROWS, WARPS = G::WARPS, SLOTS = G::SLOTS, ALL = WARPS + 1;
   constexpr int NQ = D / 16;   // MMA steps over the head dimension
   constexpr int NV = D / 16;   // 16-row blocks of V^T
   extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ int64_t s_sum[2][kWarps];
-  __shared__ int s_long[kWarps];
-  __shared__ Start s_start;
-  __shared__ float s_m[kWarps][ROWS], s_l[kWarps][ROWS];
-  __shared__ int s_u[kWarps];
+  __shared__ __align__(8) uint64_t full_bar[SLOTS], empty_bar[SLOTS];
+  __shared__ uint2 head[SLOTS];  // exponent bytes of a slot's two halves; bit h: half h has no page
+  __shared__ int64_t s_sum[2][ALL], s_off;
+  __shared__ int s_long[ALL], s_b;
+  __shared__ float s_m[WARPS][ROWS], s_l[WARPS][ROWS];
+  __shared__ int s_u[WARPS];
+  __shared__ volatile int abort_flag;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
   const int group = p.Hq / p.Hkv;
+  if (tid == 0) {
+    for (int i = 0; i < SLOTS; ++i) {
+      mbar_init(&full_bar[i], 33);  // the copies of 32 lanes, and the slot's header
+      mbar_init(&empty_bar[i], 1);
+    }
+    abort_flag = 0;
+    fence_mbar_init();
+  }
   pdl_wait();
   pdl_trigger();
 
   // ---- the CTA's range of the work: units if some sequence is longer than
-  // kWholeUnits, else whole sequences (nothing to join then)
-  const int per = (p.B + kThreads - 1) / kThreads;
-  const int b0 = min(tid * per, p.B), b1 = min(b0 + per, p.B);
-  int64_t seqs = 0, units = 0;
-  int longest = 0;
-  for (int b = b0; b < b1; ++b) {
-    const Request r = get_request(p, b);
-    const int tiles = (int)(((int64_t)r.n * group + ROWS - 1) / ROWS), ku = units_of(r.kv);
-    seqs += (int64_t)tiles * p.Hkv;
-    units += (int64_t)tiles * p.Hkv * ku;
-    if (tiles) longest = max(longest, ku);
-    if (blockIdx.x == 0 && r.bad) report_status(p.dev_status, NVFP4_E_BAD_PAGE);
-  }
-  int64_t in_s = seqs, in_u = units;
-#pragma unroll
-  for (int d = 1; d < 32; d <<= 1) {
-    const int64_t a = __shfl_up_sync(0xFFFFFFFFu, in_s, d), c = __shfl_up_sync(0xFFFFFFFFu, in_u, d);
-    if (lane >= d) {
-      in_s += a;
-      in_u += c;
-    }
-    longest = max(longest, __shfl_xor_sync(0xFFFFFFFFu, longest, d));
-  }
-  if (lane == 31) {
-    s_sum[0][warp] = in_s;
-    s_sum[1][warp] = in_u;
-    s_long[warp] = longest;
-  }
-  __syncthreads();
-  longest = max(max(s_long[0], s_long[1]), max(s_long[2], s_long[3]));
-  const bool split = longest > kWholeUnits;
-  int64_t total = 0, before = split ? in_u - units : in_s - seqs;
-  for (int w = 0; w < kWarps; ++w) {
-    const int64_t x = s_sum[split ? 1 : 0][w];
-    total += x;
-    if (w < warp) before += x;
-  }
-  const int64_t lo = total * blockIdx.x / gridDim.x, hi = total * (blockIdx.x + 1) / gridDim.x;
-  if (lo < hi && before <= lo && lo < before + (split ? units : seqs)) {
+  // kWholeKeys, else whole sequences (nothing to join then)
+  P it;
+  {
+    const int per = (p.B + G::THREADS - 1) / G::THREADS;
+    const int b0 = min(tid * per, p.B), b1 = min(b0 + per, p.B);
+    int64_t seqs = 0, units = 0;
+    int longest = 0;
     for (int b = b0; b < b1; ++b) {
       const Request r = get_request(p, b);
-      const int64_t w = ((int64_t)r.n * group + ROWS - 1) / ROWS * p.Hkv * (split ? units_of(r.kv) : 1);
-      if (lo < before + w) {
-        s_start.b = b;
-        s_start.off = lo - before;
-        break;
+      const int64_t n = P::row_tiles(r.n, group) * p.Hkv;
+      seqs += n;
+      units += n * P::units(r.kv);
+      if (n) longest = max(longest, r.kv);
+      if (blockIdx.x == 0 && r.bad) report_status(p.dev_status, NVFP4_E_BAD_PAGE);
+    }
+    int64_t in_s = seqs, in_u = units;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int64_t a = __shfl_up_sync(0xFFFFFFFFu, in_s, d), c = __shfl_up_sync(0xFFFFFFFFu, in_u, d);
+      if (lane >= d) {
+        in_s += a;
+        in_u += c;
       }
-      before += w;
+      longest = max(longest, __shfl_xor_sync(0xFFFFFFFFu, longest, d));
     }
-  }
-  __syncthreads();
-  if (blockIdx.x == 0 && tid == 0) *p.total = total;
-  if (lo >= hi) {
-    if (tid == 0) p.cut[blockIdx.x].before = 0;
-    return;
-  }
-  int b = s_start.b;
-  int64_t off = s_start.off, pos = lo;
-
-  uint8_t* ring = smem + warp * G::WARP_BYTES;
-  const uint32_t ring_u = smem_u32(ring);
-  uint2* head = reinterpret_cast<uint2*>(smem + G::RING_BYTES) + warp * kStages * 2;
-  const int S = 1 << p.shift;
-  bool first = true;
-
-  while (pos < hi && b < p.B) {
-    const Request rq = get_request(p, b);
-    const int rows = rq.n * group, tiles = (rows + ROWS - 1) / ROWS, ku = units_of(rq.kv), span = split ? ku : 1;
-    if (off >= (int64_t)tiles * p.Hkv * span) {
-      ++b;
-      off = 0;
-      continue;
+    if (lane == 31) {
+      s_sum[0][warp] = in_s;
+      s_sum[1][warp] = in_u;
+      s_long[warp] = longest;
     }
-    const int seq = (int)(off / span), u0 = (int)(off % span);
-    const int take = (int)min((int64_t)(span - u0), hi - pos);
-    const int hk = seq / tiles, row0 = (seq % tiles) * ROWS;
-    const int nrows = min(ROWS, rows - row0);
-    if (first && tid == 0) {
-      p.cut[blockIdx.x] = {split ? u0 : 0, span, rq.q0 * group + row0, hk, nrows, {0, 0, 0}};
+    __syncthreads();
+    for (int w = 0; w < ALL; ++w) longest = max(longest, s_long[w]);
+    it.split = longest > kWholeKeys;
+    int64_t total = 0, before = it.split ? in_u - units : in_s - seqs;
+    for (int w = 0; w < ALL; ++w) {
+      const int64_t x = s_sum[it.split ? 1 : 0][w];
+      total += x;
+      if (w < warp) before += x;
     }
-    // keys that the last row of the tile sees
-    const int limit = min(rq.kv, rq.kv - rq.n + (row0 + nrows - 1) / group + 1);
-    const int t0 = split ? u0 * kWarps : 0;
-    const int t1 = min(split ? (u0 + take) * kWarps : INT32_MAX, limit > 0 ? (limit + kTile - 1) / kTile : 0);
-    const int nt = t1 - t0 - warp > 0 ? (t1 - t0 - warp + kWarps - 1) / kWarps : 0;  // this warp's tiles
-
-    // pages of 32 of the warp's tiles at a time, one (or two, of 16 keys) per
-    // lane: ids, -1 where there is none, and the exponent bytes
-    int page_a = -1, page_b = -1;
-    uint32_t exps = 0;
-    auto load_pages = [&](int j) {
-      page_a = page_b = -1;
-      exps = 0;
-      if (j + lane < nt) {
-        const int key = (t0 + warp + (j + lane) * kWarps) * kTile;
-        const int64_t row = b * p.ld_table;
-        page_a = p.table[row + (key >> p.shift)];
-        page_b = p.shift == 4 && key + 16 < limit ? p.table[row + (key >> p.shift) + 1] : page_a;
-        if (page_a < 0 || page_a >= p.num_pages) {
-          page_a = -1;
-          report_status(p.dev_status, NVFP4_E_BAD_PAGE);
+    it.pos = total * blockIdx.x / gridDim.x;
+    it.hi = total * (blockIdx.x + 1) / gridDim.x;
+    if (it.pos < it.hi && before <= it.pos && it.pos < before + (it.split ? units : seqs)) {
+      for (int b = b0; b < b1; ++b) {
+        const Request r = get_request(p, b);
+        const int64_t w = P::row_tiles(r.n, group) * p.Hkv * (it.split ? P::units(r.kv) : 1);
+        if (it.pos < before + w) {
+          s_b = b;
+          s_off = it.pos - before;
+          break;
         }
-        if (page_b < 0 || page_b >= p.num_pages) {
-          page_b = -1;
-          report_status(p.dev_status, NVFP4_E_BAD_PAGE);
-        }
-        if (page_a >= 0) {
-          const int64_t at = (int64_t)page_a * p.Hkv + hk;
-          exps = p.k_exps[at] | (uint32_t)p.v_exps[at] << 8;
-        }
-        if (page_b >= 0) {
-          const int64_t at = (int64_t)page_b * p.Hkv + hk;
-          exps |= (uint32_t)p.k_exps[at] << 16 | (uint32_t)p.v_exps[at] << 24;
-        }
+        before += w;
       }
-    };
-    // copies of tile j into ring slot s
-    auto issue = [&](int j, int s) {
-      if (j < nt) {
-        if ((j & 31) == 0) load_pages(j);
-        const int pa = __shfl_sync(0xFFFFFFFFu, page_a, j & 31), pb = __shfl_sync(0xFFFFFFFFu, page_b, j & 31);
-        const uint32_t ex = __shfl_sync(0xFFFFFFFFu, exps, j & 31);
-        if (lane == 0) head[s * 2] = make_uint2(ex, (pa < 0 ? 1u : 0u) | (pb < 0 ? 2u : 0u));
-        const int key0 = (t0 + warp + j * kWarps) * kTile;
+    }
+    __syncthreads();
+    if (blockIdx.x == 0 && tid == 0) *p.total = total;
+    if (it.pos >= it.hi) {
+      if (tid == 0) p.cut[blockIdx.x].before = 0;
+      return;
+    }
+    it.b = s_b;
+    it.off = s_off;
+  }
+
+  if (warp == WARPS) {
+    // ------------------------------------------------------------ copies
+    const int S = 1 << p.shift;
+    int slot = 0;
+    uint32_t phase = 1;
+    bool ok = true;
+    while (ok && it.next(p, group)) {
+      const int32_t* table = p.table + it.b * p.ld_table;
+      int page_a = -1, page_b = -1;  // of 32 tiles, one per lane (two pages where they hold 16 keys)
+      uint32_t exps = 0;
+      for (int tile = it.t0; tile < it.t1; ++tile) {
+        const int j = (tile - it.t0) & 31;
+        if (j == 0) {
+          page_a = page_b = -1;
+          exps = 0;
+          if (tile + lane < it.t1) {
+            const int key = (tile + lane) * kTile;
+            page_a = table[key >> p.shift];
+            page_b = p.shift == 4 && key + 16 < it.limit ? table[(key >> p.shift) + 1] : page_a;
+            if (page_a < 0 || page_a >= p.num_pages) page_a = -1;
+            if (page_b < 0 || page_b >= p.num_pages) page_b = -1;
+            if (page_a < 0 || page_b < 0) report_status(p.dev_status, NVFP4_E_BAD_PAGE);
+            if (page_a >= 0) {
+              const int64_t at = (int64_t)page_a * p.Hkv + it.hk;
+              exps = p.k_exps[at] | (uint32_t)p.v_exps[at] << 8;
+            }
+            if (page_b >= 0) {
+              const int64_t at = (int64_t)page_b * p.Hkv + it.hk;
+              exps |= (uint32_t)p.k_exps[at] << 16 | (uint32_t)p.v_exps[at] << 24;
+            }
+          }
+        }
+        const int pa = __shfl_sync(0xFFFFFFFFu, page_a, j), pb = __shfl_sync(0xFFFFFFFFu, page_b, j);
+        if (!warp_wait(&empty_bar[slot], phase, &abort_flag, p.dev_status)) {
+          ok = false;
+          break;
+        }
+        const int key0 = tile * kTile;
         constexpr int CPR = D / 16;          // 16-byte chunks of a row
         constexpr int RPI = 32 / CPR;        // rows of a warp's copy
-        const int64_t ba = ((int64_t)max(pa, 0) * p.Hkv + hk) << p.shift;
-        const int64_t bb = ((int64_t)max(pb, 0) * p.Hkv + hk) << p.shift;
-        const uint32_t base = ring_u + s * G::STAGE_BYTES;
+        const int64_t ba = ((int64_t)max(pa, 0) * p.Hkv + it.hk) << p.shift;
+        const int64_t bb = ((int64_t)max(pb, 0) * p.Hkv + it.hk) << p.shift;
+        const uint32_t base = smem_u32(smem) + slot * G::SLOT_BYTES;
 #pragma unroll
         for (int i = 0; i < kTile / RPI; ++i) {
           const int r = i * RPI + lane / CPR, c = lane % CPR, key = key0 + r;
-          const bool second = r >= 16;
-          const bool valid = key < limit && (second ? pb : pa) >= 0;
-          const int64_t at = ((second ? bb : ba) + (key & (S - 1))) * D + c * 16;
+          const bool valid = key < it.limit && (r >= 16 ? pb : pa) >= 0;
+          const int64_t at = ((r >= 16 ? bb : ba) + (key & (S - 1))) * D + c * 16;
           const uint32_t dst = base + tile_offset<D>(r, c);
           cp_async16(dst, p.k_codes + at, valid);
           cp_async16(dst + G::TILE_BYTES, p.v_codes + at, valid);
         }
+        cp_async_arrive(&full_bar[slot]);
+        const uint32_t ex = __shfl_sync(0xFFFFFFFFu, exps, j);
+        if (lane == 0) {
+          head[slot] = make_uint2(ex, (pa < 0 ? 1u : 0u) | (pb < 0 ? 2u : 0u));
+          asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(&full_bar[slot])) : "memory");
+        }
+        if (++slot == SLOTS) {
+          slot = 0;
+          phase ^= 1;
+        }
       }
-      cp_async_commit();
-    };
-#pragma unroll
-    for (int s = 0; s < kStages - 1; ++s) issue(s, s);
+    }
+    cp_async_wait_all();
+    return;
+  }
 
-    // ---- query rows: lane (g, t) holds row g's elements for its keys' chunks,
-    // as f16 times the row's power of two
+  // -------------------------------------------------------------- arithmetic
+  int slot = warp % SLOTS;      // of this warp's next tile
+  uint32_t phase = 0;
+  int turn = warp;              // tiles of the CTA until this warp's next one
+  bool first = true, ok = true;
+  while (it.next(p, group)) {
+    if (first && tid == 0)
+      p.cut[blockIdx.x] = {it.split ? it.u0 : 0, it.span, it.rq.q0 * group + it.row0, it.hk, it.nrows, {0, 0, 0}};
+
+    // query rows: lane (g, t) holds row g's elements for its keys' chunks, as
+    // f16 times the row's power of two
     uint32_t qf[NT][NQ][2];
     float qs[NT][2];     // log2 logit per accumulator unit, rows 2t and 2t + 1
     int lim[NT][2];      // keys that the row sees
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
-      const int r = row0 + n * 8 + g;
+      const int r = it.row0 + n * 8 + g;
       float v[D / 4], amax = 0.0f;
       const __nv_bfloat16* src =
-          p.q + (int64_t)(rq.q0 + r / group) * p.ld_q + (int64_t)(hk * group + r % group) * D + 16 * t;
+          p.q + (int64_t)(it.rq.q0 + r / group) * p.ld_q + (int64_t)(it.hk * group + r % group) * D + 16 * t;
 #pragma unroll
       for (int h = 0; h < D / 64; ++h) {
         uint4 w[2] = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
-        if (r < rows) {
+        if (r < it.rows) {
           w[0] = *reinterpret_cast<const uint4*>(src + 64 * h);
           w[1] = *reinterpret_cast<const uint4*>(src + 64 * h + 8);
         }
@@ -344,11 +393,11 @@ __global__ void __launch_bounds__(kThreads, (Geo<D, NT>::CTAS)) kv_attention_ker
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
         qs[n][c] = __shfl_sync(0xFFFFFFFFu, rs, (2 * t + c) * 4);
-        const int rr = row0 + n * 8 + 2 * t + c;
-        lim[n][c] = rr < rows ? min(rq.kv, rq.kv - rq.n + rr / group + 1) : 0;
+        const int rr = it.row0 + n * 8 + 2 * t + c;
+        lim[n][c] = rr < it.rows ? min(it.rq.kv, it.rq.kv - it.rq.n + rr / group + 1) : 0;
       }
     }
-    const int all_see = rq.kv - rq.n + row0 / group + 1;  // keys below this are seen by every row
+    const int all_see = it.rq.kv - it.rq.n + it.row0 / group + 1;  // keys below this are seen by every row
 
     float o[NT][NV][4], m[NT][2], l[NT][2];
 #pragma unroll
@@ -360,15 +409,13 @@ __global__ void __launch_bounds__(kThreads, (Geo<D, NT>::CTAS)) kv_attention_ker
     }
     int unit_exp = -127;  // outputs are held in units of 2^unit_exp, the largest value exponent so far
 
-    int slot = 0;
-    for (int j = 0; j < nt; ++j) {
-      cp_async_wait<kStages - 2>();
-      __syncwarp();
-      issue(j + kStages - 1, slot == 0 ? kStages - 1 : slot - 1);
-      const uint2 hd = head[slot * 2];
-      const uint8_t* kt = ring + slot * G::STAGE_BYTES;
+    int tile = it.t0 + turn;
+    for (; tile < it.t1; tile += WARPS) {
+      ok = ok && warp_wait(&full_bar[slot], phase, &abort_flag, p.dev_status);
+      const uint2 hd = head[slot];
+      const uint8_t* kt = smem + slot * G::SLOT_BYTES;
       const uint8_t* vt = kt + G::TILE_BYTES;
-      const int key0 = (t0 + warp + j * kWarps) * kTile;
+      const int key0 = tile * kTile;
 
       // S^T = K Q^T, two blocks of 16 keys
       float s[NT][2][4];
@@ -392,13 +439,14 @@ __global__ void __launch_bounds__(kThreads, (Geo<D, NT>::CTAS)) kv_attention_ker
         }
       }
       // logits in log2 units; keys that a row does not see are -inf
-      const float ks[2] = {exp2_int((int)(hd.x & 255) - 127), exp2_int((int)(hd.x >> 16 & 255) - 127)};
 #pragma unroll
-      for (int n = 0; n < NT; ++n)
+      for (int kb = 0; kb < 2; ++kb) {
+        const float ks = exp2_int((int)(hd.x >> (16 * kb) & 255) - 127);
 #pragma unroll
-        for (int kb = 0; kb < 2; ++kb)
+        for (int n = 0; n < NT; ++n)
 #pragma unroll
-          for (int c = 0; c < 4; ++c) s[n][kb][c] = s[n][kb][c] * qs[n][c & 1] * ks[kb];
+          for (int c = 0; c < 4; ++c) s[n][kb][c] = s[n][kb][c] * qs[n][c & 1] * ks;
+      }
       if (key0 + kTile > all_see || hd.y) {
 #pragma unroll
         for (int n = 0; n < NT; ++n)
@@ -444,12 +492,14 @@ __global__ void __launch_bounds__(kThreads, (Geo<D, NT>::CTAS)) kv_attention_ker
           pf[n][kb][0] = transpose8x8(pack_f16(s[n][kb][0], s[n][kb][1]));
           pf[n][kb][1] = transpose8x8(pack_f16(s[n][kb][2], s[n][kb][3]));
         }
+        if (__any_sync(0xFFFFFFFFu, f[0] != 1.0f || f[1] != 1.0f)) {
 #pragma unroll
-        for (int i = 0; i < NV; ++i) {
-          o[n][i][0] *= f[0];
-          o[n][i][1] *= f[1];
-          o[n][i][2] *= f[0];
-          o[n][i][3] *= f[1];
+          for (int i = 0; i < NV; ++i) {
+            o[n][i][0] *= f[0];
+            o[n][i][1] *= f[1];
+            o[n][i][2] *= f[0];
+            o[n][i][3] *= f[1];
+          }
         }
       }
       // O^T += V^T P^T: lane (g, t) reads D / 8 elements of keys 2t, 2t+1, 2t+8, 2t+9
@@ -481,14 +531,19 @@ __global__ void __launch_bounds__(kThreads, (Geo<D, NT>::CTAS)) kv_attention_ker
             for (int n = 0; n < NT; ++n) mma16816(o[n][2 * i + h], a0, a1, a2, a3, pf[n][kb][0], pf[n][kb][1]);
           }
       }
-      slot = slot + 1 == kStages ? 0 : slot + 1;
+      __syncwarp();  // every lane has read the slot
+      if (lane == 0) asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(&empty_bar[slot])) : "memory");
+      slot += WARPS;
+      if (slot >= SLOTS) {
+        slot -= SLOTS;
+        phase ^= 1;
+      }
     }
-    cp_async_wait<0>();
-    __syncwarp();
+    turn = tile - max(it.t1, it.t0);
 
-    // ---- join the four warps: lane (g, t) holds D / 8 consecutive elements,
-    // from g * D / 8, of rows 2t and 2t + 1
-    float* ow = reinterpret_cast<float*>(ring);
+    // ---- join the warps: lane (g, t) holds D / 8 consecutive elements, from
+    // g * D / 8, of rows 2t and 2t + 1
+    float* join = reinterpret_cast<float*>(smem + G::RING_BYTES);
     constexpr int EL = D / 8;
 #pragma unroll
     for (int n = 0; n < NT; ++n)
@@ -503,30 +558,34 @@ __global__ void __launch_bounds__(kThreads, (Geo<D, NT>::CTAS)) kv_attention_ker
           s_m[warp][r] = m[n][c];
           s_l[warp][r] = sum;
         }
+        // four elements at a time, permuted within the row so that the lanes of
+        // an access and the threads that read it spread over the banks
 #pragma unroll
         for (int i = 0; i < EL / 4; ++i)
-          *reinterpret_cast<float4*>(ow + r * D + g * EL + 4 * i) =
+          *reinterpret_cast<float4*>(join + (warp * ROWS + r) * D + (((g * EL / 4 + i) ^ g ^ (t << 1)) << 2)) =
               make_float4(o[n][2 * i][c], o[n][2 * i][c + 2], o[n][2 * i + 1][c], o[n][2 * i + 1][c + 2]);
       }
     if (lane == 0) s_u[warp] = unit_exp;
-    __syncthreads();
-    const bool whole = take == span;
+    asm volatile("bar.sync 1, %0;" ::"n"(WARPS * 32) : "memory");
+    const bool whole = it.take == it.span;
     const int64_t part = (int64_t)blockIdx.x * 2 + (first ? 0 : 1);
-    const int umax = max(max(s_u[0], s_u[1]), max(s_u[2], s_u[3]));
+    int umax = s_u[0];
+#pragma unroll
+    for (int w = 1; w < WARPS; ++w) umax = max(umax, s_u[w]);
     constexpr int TPR = D / 4;  // threads of a row, four elements each
-    for (int r = tid / TPR; r < nrows; r += kThreads / TPR) {
-      const int d = tid % TPR * 4;
+    for (int r = tid / TPR; r < it.nrows; r += WARPS * 32 / TPR) {
+      const int d4 = tid % TPR, d = d4 * 4, at4 = (d4 ^ (d4 / (EL / 4)) ^ (r & 6)) << 2;
       float mx = -INFINITY;
 #pragma unroll
-      for (int w = 0; w < kWarps; ++w) mx = fmaxf(mx, s_m[w][r]);
+      for (int w = 0; w < WARPS; ++w) mx = fmaxf(mx, s_m[w][r]);
       const float ms = mx == -INFINITY ? 0.0f : mx;
       float sum = 0.0f;
       float4 acc = make_float4(0, 0, 0, 0);
 #pragma unroll
-      for (int w = 0; w < kWarps; ++w) {
+      for (int w = 0; w < WARPS; ++w) {
         const float f = ex2(s_m[w][r] - ms), fu = f * exp2_int(max(s_u[w] - umax, -127));
         sum += s_l[w][r] * f;
-        const float4 x = *reinterpret_cast<const float4*>(smem + w * G::WARP_BYTES + (r * D + d) * 4);
+        const float4 x = *reinterpret_cast<const float4*>(join + (w * ROWS + r) * D + at4);
         acc.x += x.x * fu, acc.y += x.y * fu, acc.z += x.z * fu, acc.w += x.w * fu;
       }
       const bool none = sum == 0.0f;
@@ -535,8 +594,8 @@ __global__ void __launch_bounds__(kThreads, (Geo<D, NT>::CTAS)) kv_attention_ker
                  : make_float4(acc.x * inv * us, acc.y * inv * us, acc.z * inv * us, acc.w * inv * us);
       const float lse2 = none ? -INFINITY : mx + (log2f(sum) - kBoost);
       if (whole) {
-        const int rr = row0 + r;
-        const int64_t at = (int64_t)(rq.q0 + rr / group) * p.Hq + hk * group + rr % group;
+        const int rr = it.row0 + r;
+        const int64_t at = (int64_t)(it.rq.q0 + rr / group) * p.Hq + it.hk * group + rr % group;
         const __nv_bfloat162 lo2 = __floats2bfloat162_rn(acc.x, acc.y), hi2 = __floats2bfloat162_rn(acc.z, acc.w);
         *reinterpret_cast<uint2*>(p.out + at * D + d) =
             make_uint2(*reinterpret_cast<const uint32_t*>(&lo2), *reinterpret_cast<const uint32_t*>(&hi2));
@@ -546,10 +605,8 @@ __global__ void __launch_bounds__(kThreads, (Geo<D, NT>::CTAS)) kv_attention_ker
         if (d == 0) p.part_lse[part * ROWS + r] = lse2;
       }
     }
-    __syncthreads();  // the ring is free again
+    asm volatile("bar.sync 1, %0;" ::"n"(WARPS * 32) : "memory");  // the join buffer is free again
     first = false;
-    pos += take;
-    off += take;
   }
 }
 
@@ -642,9 +699,9 @@ cudaError_t launch(const KvAttention& a, cudaStream_t st) {
   cudaError_t e = ensure_dynamic_smem(reinterpret_cast<const void*>(kv_attention_kernel<D, NT>), G::SMEM_BYTES);
   if (e != cudaSuccess) return e;
   const int ctas = num_sms() * G::CTAS;
-  e = launch_pdl(kv_attention_kernel<D, NT>, ctas, kThreads, G::SMEM_BYTES, st, p);
+  e = launch_pdl(kv_attention_kernel<D, NT>, ctas, G::THREADS, G::SMEM_BYTES, st, p);
   // a table that holds no sequence long enough to be split needs no join
-  if (e != cudaSuccess || (int64_t)a.M * a.page_size <= kWholeUnits * kUnit) return e;
+  if (e != cudaSuccess || (int64_t)a.M * a.page_size <= kWholeKeys) return e;
   return launch_pdl(kv_attention_join_kernel<D, NT>, dim3(ctas - 1, G::ROWS / 4), 128, 0, st, p, ctas);
 }
 
