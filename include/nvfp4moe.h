@@ -608,8 +608,8 @@ int kv_append(const void* k, const void* v, int x_dtype, int64_t ld_k, int64_t l
  * of its request and call.  Rows of out past query_start[B] are not written.
  * The result does not depend on the other requests of the call, except that
  * their lengths move the points at which partial sums are joined.
- * Constraints: Hq % Hkv == 0, ld_q >= Hq * D, ld_q % 8 == 0, M >= 1, T * Hq < 2^31,
- * 0 <= B <= 8192.
+ * Constraints: Hq % Hkv == 0, ld_q >= Hq * D, ld_q % 8 == 0, M >= 1, P >= 1,
+ * T * Hq and P * Hkv < 2^31, 0 <= B <= 8192.
  * ------------------------------------------------------------------------ */
 size_t kv_attention_workspace_bytes(int T, int B, int Hq, int Hkv, int D);
 int kv_attention(const void* q, int64_t ld_q, const uint8_t* k_codes, const uint8_t* k_exps, const uint8_t* v_codes,

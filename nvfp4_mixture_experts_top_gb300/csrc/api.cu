@@ -796,10 +796,11 @@ int kv_attention(const void* q, int64_t ld_q, const uint8_t* k_codes, const uint
                  size_t workspace_bytes, nvfp4_stream_t stream) {
   if (T < 0 || B < 0 || Hq <= 0 || Hkv <= 0 || M < 0 || num_pages < 0 || max_query_len < 0) return NVFP4_E_INVAL;
   if ((D != 64 && D != 128) || !page_size_ok(page_size) || Hq % Hkv != 0 || B > kMaxKvRequests || M < 1 ||
-      ld_table < M || num_pages > INT32_MAX / page_size)
+      ld_table < M || num_pages > INT32_MAX / page_size || num_pages * Hkv > INT32_MAX)
     return NVFP4_E_SHAPE;
   if (ld_q < (int64_t)Hq * D || ld_q % 8 != 0 || (int64_t)T * Hq > INT32_MAX) return NVFP4_E_SHAPE;
   if (T == 0 || B == 0) return NVFP4_OK;
+  if (num_pages == 0) return NVFP4_E_SHAPE;
   if (q == nullptr || k_codes == nullptr || k_exps == nullptr || v_codes == nullptr || v_exps == nullptr ||
       block_table == nullptr || kv_lens == nullptr || query_start == nullptr || out == nullptr)
     return NVFP4_E_INVAL;

@@ -36,5 +36,16 @@ __device__ __forceinline__ uint32_t rescale_codes(uint32_t w, float f) {
   return encode4(a.x * f, a.y * f, b.x * f, b.y * f);
 }
 
+// TMA load of a 3-D box by one elected lane of a converged warp.
+__device__ __forceinline__ void ew_tma_load_3d(void* smem_dst, const void* tmap, uint64_t* bar, int32_t x, int32_t y,
+                                               int32_t z) {
+  asm volatile(
+      "{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t"
+      "@e cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3, %4}], [%5];\n\t}" ::"r"(smem_u32(smem_dst)),
+      "l"(tmap), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar))
+      : "memory");
+}
+
 }  // namespace kv
 }  // namespace nvfp4moe

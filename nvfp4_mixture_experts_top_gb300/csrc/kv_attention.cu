@@ -11,9 +11,9 @@
 //    result, and a small second kernel joins them in order (no atomics: the
 //    result repeats bit for bit);
 //  - one warp of a CTA does nothing but page lookups and copies: it fills a
-//    ring of 32-key tiles (cp.async, an mbarrier per slot) and runs ahead of the
-//    arithmetic across the ends of sequences; the other warps take tiles in
-//    turn, each with its own running maximum, sum and output;
+//    ring of 32-key tiles by TMA and runs ahead of the arithmetic across the
+//    ends of sequences; the other warps take tiles in turn, each with its own
+//    running maximum, sum and output;
 //  - arithmetic is mma.sync m16n8k16 on f16 with fp32 accumulation: every E4M3
 //    value is an f16 value, and a query row is carried as f16 with its own
 //    power of two.  Keys (and the head dimension of V) are the 16-row side and
@@ -22,9 +22,12 @@
 //    less than a tenth of its rate.
 // Softmax statistics and outputs are fp32.  Weights are rounded to f16 after a
 // shift by 2^12 (so that they keep 11 bits down to 2^-26 of the largest).
+#include <cuda.h>
+
 #include "common.cuh"
 #include "kernels.h"
 #include "kv.cuh"
+#include "tmap.h"
 
 namespace nvfp4moe {
 namespace {
@@ -43,7 +46,7 @@ struct Cut {
 
 struct Params {
   const __nv_bfloat16* q;
-  const uint8_t *k_codes, *k_exps, *v_codes, *v_exps;
+  const uint8_t *k_exps, *v_exps;
   const int32_t *table, *kv_lens, *query_start;
   __nv_bfloat16* out;
   float* lse;
@@ -79,16 +82,6 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool valid) {
-  const int bytes = valid ? 16 : 0;  // 0: the destination is zero-filled
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
-}
-// Arrive on `bar` (once per calling thread) when this thread's copies so far have landed.
-__device__ __forceinline__ void cp_async_arrive(uint64_t* bar) {
-  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
-}
-__device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
-
 // D += A B, A [16 x 16] f16 (row), B [16 x 8] f16 (column), fp32 accumulators.
 __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
                                          uint32_t b0, uint32_t b1) {
@@ -108,14 +101,19 @@ __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 
-// Byte offset of 16-byte chunk c of key row r in a tile's [32][D] codes.  The
-// permutation makes both access patterns free of bank conflicts: keys as MMA
-// rows (lanes read rows g, chunks t and t + 4) and as MMA depth (lanes read
-// rows 2t, 2t + 1, chunk g).
+// Byte offset of 16-byte chunk c of key row r in a tile's [32][D] codes, as the
+// TMA's 128-byte (D = 64: 64-byte) swizzle places it.
 template <int D>
 __device__ __forceinline__ uint32_t tile_offset(int r, int c) {
-  if (D == 128) return r * 128 + ((c ^ (r & 6) ^ ((r & 1) << 2)) << 4);
-  return (r >> 1) * 128 + (((((r & 1) << 2) | c) ^ (r & 6)) << 4);
+  return D == 128 ? r * 128 + ((c ^ (r & 7)) << 4) : r * 64 + ((c ^ (r >> 1 & 3)) << 4);
+}
+// Key of row i (0..7) of an eight-key MMA block.  Any order of the keys gives
+// the same sums as long as K and V agree; with this one both access patterns of
+// the swizzled tile are free of bank conflicts: K (lane (g, t) reads the row of
+// key g, chunks t and t + 4) and V (rows of keys 2t and 2t + 1, chunk g).
+template <int D>
+__device__ __forceinline__ int key_of(int i) {
+  return D == 128 ? i ^ ((i & 1) << 2) : (i & 4) | ((i & 1) << 1) | ((i >> 1 ^ i) & 1);
 }
 
 template <int D, int NT>
@@ -133,7 +131,12 @@ struct Geo {
   static constexpr int SLOTS = (111 * 1024 + D * 8 - JOIN_BYTES) / SLOT_BYTES;
   static constexpr int RING_BYTES = SLOTS * SLOT_BYTES;
   static constexpr int SMEM_BYTES = RING_BYTES + JOIN_BYTES;
-  static_assert(WARPS < SLOTS, "a warp's next tile is at most one lap ahead");
+  // "full" barriers are a ring of their own, a whole number of laps of the
+  // warps: the use of a barrier before a warp's next tile is then a tile of the
+  // same warp, so the phase it waits for is never two ahead.  (With a barrier
+  // per slot it could be: copies finish out of order.)
+  static constexpr int FULLS = (SLOTS + WARPS - 1) / WARPS * WARPS;
+  static_assert(WARPS < SLOTS && FULLS <= 32, "ring sizes");
 };
 
 // The pieces of sequences that a CTA's range of the work consists of, in order.
@@ -185,29 +188,31 @@ struct Pieces {
 };
 
 template <int D, int NT>
-__global__ void __launch_bounds__((Geo<D, NT>::THREADS), (Geo<D, NT>::CTAS)) kv_attention_kernel(const Params p) {
+__global__ void __launch_bounds__((Geo<D, NT>::THREADS), (Geo<D, NT>::CTAS))
+    kv_attention_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
+                        const Params p) {
   using G = Geo<D, NT>;
   using P = Pieces<D, NT>;
-  constexpr int ROWS = G::ROWS, WARPS = G::WARPS, SLOTS = G::SLOTS, ALL = WARPS + 1;
+  constexpr int ROWS = G::ROWS, WARPS = G::WARPS, SLOTS = G::SLOTS, FULLS = G::FULLS, ALL = WARPS + 1;
   constexpr int NQ = D / 16;   // MMA steps over the head dimension
   constexpr int NV = D / 16;   // 16-row blocks of V^T
-  extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ __align__(8) uint64_t full_bar[SLOTS], empty_bar[SLOTS];
+  extern __shared__ __align__(1024) uint8_t smem[];
+  __shared__ __align__(8) uint64_t full_bar[FULLS], empty_bar[SLOTS];
   __shared__ uint2 head[SLOTS];  // exponent bytes of a slot's two halves; bit h: half h has no page
   __shared__ int64_t s_sum[2][ALL], s_off;
   __shared__ int s_long[ALL], s_b;
   __shared__ float s_m[WARPS][ROWS], s_l[WARPS][ROWS];
   __shared__ int s_u[WARPS];
   __shared__ volatile int abort_flag;
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3, kg = key_of<D>(g);
   const int group = p.Hq / p.Hkv;
   if (tid == 0) {
-    for (int i = 0; i < SLOTS; ++i) {
-      mbar_init(&full_bar[i], 33);  // the copies of 32 lanes, and the slot's header
-      mbar_init(&empty_bar[i], 1);
-    }
+    for (int i = 0; i < FULLS; ++i) mbar_init(&full_bar[i], 1);
+    for (int i = 0; i < SLOTS; ++i) mbar_init(&empty_bar[i], 1);
     abort_flag = 0;
     fence_mbar_init();
+    prefetch_tmap(&tm_k);
+    prefetch_tmap(&tm_v);
   }
   pdl_wait();
   pdl_trigger();
@@ -279,8 +284,8 @@ __global__ void __launch_bounds__((Geo<D, NT>::THREADS), (Geo<D, NT>::CTAS)) kv_
   if (warp == WARPS) {
     // ------------------------------------------------------------ copies
     const int S = 1 << p.shift;
-    int slot = 0;
-    uint32_t phase = 1;
+    int slot = 0, full = 0;
+    uint32_t phase = 1, full_phase = 0, issued = 0, issued_par = 0;
     bool ok = true;
     while (ok && it.next(p, group)) {
       const int32_t* table = p.table + it.b * p.ld_table;
@@ -314,25 +319,28 @@ __global__ void __launch_bounds__((Geo<D, NT>::THREADS), (Geo<D, NT>::CTAS)) kv_
           break;
         }
         const int key0 = tile * kTile;
-        constexpr int CPR = D / 16;          // 16-byte chunks of a row
-        constexpr int RPI = 32 / CPR;        // rows of a warp's copy
-        const int64_t ba = ((int64_t)max(pa, 0) * p.Hkv + it.hk) << p.shift;
-        const int64_t bb = ((int64_t)max(pb, 0) * p.Hkv + it.hk) << p.shift;
-        const uint32_t base = smem_u32(smem) + slot * G::SLOT_BYTES;
-#pragma unroll
-        for (int i = 0; i < kTile / RPI; ++i) {
-          const int r = i * RPI + lane / CPR, c = lane % CPR, key = key0 + r;
-          const bool valid = key < it.limit && (r >= 16 ? pb : pa) >= 0;
-          const int64_t at = ((r >= 16 ? bb : ba) + (key & (S - 1))) * D + c * 16;
-          const uint32_t dst = base + tile_offset<D>(r, c);
-          cp_async16(dst, p.k_codes + at, valid);
-          cp_async16(dst + G::TILE_BYTES, p.v_codes + at, valid);
-        }
-        cp_async_arrive(&full_bar[slot]);
+        uint8_t* dst = smem + slot * G::SLOT_BYTES;
+        const int pages = p.shift == 4 ? 2 : 1;  // boxes of a tile
+        const uint32_t bytes = p.shift == 4 ? (uint32_t)G::SLOT_BYTES / 2 : (uint32_t)G::SLOT_BYTES;
         const uint32_t ex = __shfl_sync(0xFFFFFFFFu, exps, j);
-        if (lane == 0) {
-          head[slot] = make_uint2(ex, (pa < 0 ? 1u : 0u) | (pb < 0 ? 2u : 0u));
-          asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(&full_bar[slot])) : "memory");
+        if (lane == 0) head[slot] = make_uint2(ex, (pa < 0 ? 1u : 0u) | (pb < 0 ? 2u : 0u));
+        __syncwarp();
+        ew_arrive_expect_tx(&full_bar[full], (pa >= 0 ? bytes : 0) + (pages == 2 && pb >= 0 ? bytes : 0));
+        if (pa >= 0) {
+          const int block = pa * p.Hkv + it.hk, row = key0 & (S - 1);
+          kv::ew_tma_load_3d(dst, &tm_k, &full_bar[full], 0, row, block);
+          kv::ew_tma_load_3d(dst + G::TILE_BYTES, &tm_v, &full_bar[full], 0, row, block);
+        }
+        if (pages == 2 && pb >= 0) {
+          const int block = pb * p.Hkv + it.hk;
+          kv::ew_tma_load_3d(dst + G::TILE_BYTES / 2, &tm_k, &full_bar[full], 0, 0, block);
+          kv::ew_tma_load_3d(dst + G::TILE_BYTES * 3 / 2, &tm_v, &full_bar[full], 0, 0, block);
+        }
+        issued |= 1u << full;
+        issued_par = (issued_par & ~(1u << full)) | (full_phase << full);
+        if (++full == FULLS) {
+          full = 0;
+          full_phase ^= 1;
         }
         if (++slot == SLOTS) {
           slot = 0;
@@ -340,13 +348,16 @@ __global__ void __launch_bounds__((Geo<D, NT>::THREADS), (Geo<D, NT>::CTAS)) kv_
         }
       }
     }
-    cp_async_wait_all();
+    if (!ok) {  // given up: wait for the copies in flight before the CTA's memory goes
+      for (int i = 0; i < FULLS; ++i)
+        if (issued >> i & 1) mbar_wait(&full_bar[i], issued_par >> i & 1);
+    }
     return;
   }
 
   // -------------------------------------------------------------- arithmetic
-  int slot = warp % SLOTS;      // of this warp's next tile
-  uint32_t phase = 0;
+  int slot = warp, full = warp;  // of this warp's next tile
+  uint32_t full_phase = 0;
   int turn = warp;              // tiles of the CTA until this warp's next one
   bool first = true, ok = true;
   while (it.next(p, group)) {
@@ -411,11 +422,12 @@ __global__ void __launch_bounds__((Geo<D, NT>::THREADS), (Geo<D, NT>::CTAS)) kv_
 
     int tile = it.t0 + turn;
     for (; tile < it.t1; tile += WARPS) {
-      ok = ok && warp_wait(&full_bar[slot], phase, &abort_flag, p.dev_status);
+      ok = ok && warp_wait(&full_bar[full], full_phase, &abort_flag, p.dev_status);
       const uint2 hd = head[slot];
       const uint8_t* kt = smem + slot * G::SLOT_BYTES;
       const uint8_t* vt = kt + G::TILE_BYTES;
       const int key0 = tile * kTile;
+      const bool ragged = key0 + kTile > it.limit || hd.y;
 
       // S^T = K Q^T, two blocks of 16 keys
       float s[NT][2][4];
@@ -425,8 +437,8 @@ __global__ void __launch_bounds__((Geo<D, NT>::THREADS), (Geo<D, NT>::CTAS)) kv_
         for (int n = 0; n < NT; ++n) s[n][kb][0] = s[n][kb][1] = s[n][kb][2] = s[n][kb][3] = 0.0f;
 #pragma unroll
         for (int h = 0; h < D / 64; ++h) {
-          const uint4 ka = *reinterpret_cast<const uint4*>(kt + tile_offset<D>(kb * 16 + g, h * 4 + t));
-          const uint4 kc = *reinterpret_cast<const uint4*>(kt + tile_offset<D>(kb * 16 + g + 8, h * 4 + t));
+          const uint4 ka = *reinterpret_cast<const uint4*>(kt + tile_offset<D>(kb * 16 + kg, h * 4 + t));
+          const uint4 kc = *reinterpret_cast<const uint4*>(kt + tile_offset<D>(kb * 16 + kg + 8, h * 4 + t));
           const uint32_t wa[4] = {ka.x, ka.y, ka.z, ka.w}, wc[4] = {kc.x, kc.y, kc.z, kc.w};
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
@@ -454,7 +466,7 @@ __global__ void __launch_bounds__((Geo<D, NT>::THREADS), (Geo<D, NT>::CTAS)) kv_
           for (int kb = 0; kb < 2; ++kb)
 #pragma unroll
             for (int c = 0; c < 4; ++c)
-              if (key0 + kb * 16 + g + (c >> 1) * 8 >= lim[n][c & 1] || (hd.y >> kb & 1)) s[n][kb][c] = -INFINITY;
+              if (key0 + kb * 16 + kg + (c >> 1) * 8 >= lim[n][c & 1] || (hd.y >> kb & 1)) s[n][kb][c] = -INFINITY;
       }
       // value exponents of the two blocks relative to the largest so far
       const int va = hd.y & 1 ? -127 : (int)(hd.x >> 8 & 255) - 127, vb = hd.y & 2 ? -127 : (int)(hd.x >> 24) - 127;
@@ -509,13 +521,18 @@ __global__ void __launch_bounds__((Geo<D, NT>::THREADS), (Geo<D, NT>::CTAS)) kv_
         uint32_t w[4][NW];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const int r = kb * 16 + 2 * t + (i & 1) + (i >> 1) * 8;
+          const int r = kb * 16 + key_of<D>(2 * t + (i & 1)) + (i >> 1) * 8;
           if constexpr (D == 128) {
             const uint4 x = *reinterpret_cast<const uint4*>(vt + tile_offset<D>(r, g));
             w[i][0] = x.x, w[i][1] = x.y, w[i][2] = x.z, w[i][3] = x.w;
           } else {
             const uint2 x = *reinterpret_cast<const uint2*>(vt + tile_offset<D>(r, g >> 1) + (g & 1) * 8);
             w[i][0] = x.x, w[i][1] = x.y;
+          }
+          // rows past the sequence hold anything, and 0 * NaN would spread
+          if (ragged && (key0 + r >= it.limit || (hd.y >> kb & 1))) {
+#pragma unroll
+            for (int k = 0; k < NW; ++k) w[i][k] = 0;
           }
         }
 #pragma unroll
@@ -534,9 +551,11 @@ __global__ void __launch_bounds__((Geo<D, NT>::THREADS), (Geo<D, NT>::CTAS)) kv_
       __syncwarp();  // every lane has read the slot
       if (lane == 0) asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(&empty_bar[slot])) : "memory");
       slot += WARPS;
-      if (slot >= SLOTS) {
-        slot -= SLOTS;
-        phase ^= 1;
+      if (slot >= SLOTS) slot -= SLOTS;
+      full += WARPS;
+      if (full >= FULLS) {
+        full = warp;
+        full_phase ^= 1;
       }
     }
     turn = tile - max(it.t1, it.t0);
@@ -610,16 +629,17 @@ __global__ void __launch_bounds__((Geo<D, NT>::THREADS), (Geo<D, NT>::CTAS)) kv_
   }
 }
 
-// Joins the partial results of a sequence, a warp per row, parts in order.  CTA
-// c = blockIdx.x + 1 takes the sequence that its range starts in, if no earlier
-// range starts inside it.
+// Joins the partial results of a sequence, a CTA per row: CTA (c - 1, r) takes
+// row r of the sequence that the range of CTA c starts in, if no range before c
+// starts inside it.  Its four warps take parts in turn.
 template <int D, int NT>
 __global__ void __launch_bounds__(128) kv_attention_join_kernel(const Params p, int ctas) {
   constexpr int ROWS = Geo<D, NT>::ROWS;
   constexpr int E = D / 32;
+  __shared__ float s_acc[4][D], s_top[4], s_sum[4];
   pdl_wait();
   pdl_trigger();
-  const int c = blockIdx.x + 1, lane = threadIdx.x & 31, r = blockIdx.y * 4 + (threadIdx.x >> 5);
+  const int c = blockIdx.x + 1, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, r = blockIdx.y;
   const Cut cut = p.cut[c];
   if (cut.before == 0 || r >= cut.rows) return;
   const int64_t W = *p.total;
@@ -628,40 +648,65 @@ __global__ void __launch_bounds__(128) kv_attention_join_kernel(const Params p, 
   const int64_t a = W * c / ctas - cut.before, e = a + cut.span;
   const int c0 = owner(a);
   if (owner(a + cut.before - 1) != c0) return;
-  // a part per CTA; with fewer units than CTAs, a part per unit
+  // a part per CTA, or with fewer units than CTAs a part per unit; a CTA's
+  // first piece is its part 0, its last one its part 1
   const int n = W >= ctas ? owner(e - 1) - c0 + 1 : cut.span;
+  const int first = c0 * 2 + (W * c0 / ctas >= a ? 0 : 1);
   auto row_of = [&](int k) {
-    const int64_t cta = W >= ctas ? c0 + k : owner(a + k);
-    return (cta * 2 + (W * cta / ctas >= a ? 0 : 1)) * ROWS + r;
+    const int part = k == 0 ? first : (W >= ctas ? c0 + k : owner(a + k)) * 2;
+    return (int64_t)part * ROWS + r;
   };
-  float top = -INFINITY;
-  for (int k = lane; k < n; k += 32) top = fmaxf(top, p.part_lse[row_of(k)]);
+  float top = -INFINITY, sum = 0.0f, acc[E] = {};
+  for (int k0 = warp; k0 < n; k0 += 128) {  // lane i: part k0 + 4 i
+    const int m = min(32, (n - k0 + 3) / 4);
+    const int64_t row = row_of(min(k0 + 4 * lane, n - 1));
+    const float z = lane < m ? p.part_lse[row] : -INFINITY;
+    float mx = z;
 #pragma unroll
-  for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, d));
-  const float ms = top == -INFINITY ? 0.0f : top;
-  float sum = 0.0f, acc[E] = {};
-  for (int k0 = 0; k0 < n; k0 += 32) {
-    const int64_t row = row_of(min(k0 + lane, n - 1));
-    const float w = k0 + lane < n ? ex2(p.part_lse[row] - ms) : 0.0f;
-    sum += w;
-    const int m = min(32, n - k0);
+    for (int d = 16; d > 0; d >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, d));
+    const float t1 = fmaxf(top, mx), ms = t1 == -INFINITY ? 0.0f : t1, f = ex2(top - ms), w = ex2(z - ms);
+    top = t1;
+    sum = sum * f + w;
+#pragma unroll
+    for (int i = 0; i < E; ++i) acc[i] *= f;
 #pragma unroll 8
     for (int k = 0; k < m; ++k) {
       const float wk = __shfl_sync(0xFFFFFFFFu, w, k);
       const float* src = p.part + __shfl_sync(0xFFFFFFFFu, row, k) * D + lane * E;
+      float x[E];
+      if constexpr (E == 4) {
+        const float4 y = *reinterpret_cast<const float4*>(src);
+        x[0] = y.x, x[1] = y.y, x[2] = y.z, x[3] = y.w;
+      } else {
+        const float2 y = *reinterpret_cast<const float2*>(src);
+        x[0] = y.x, x[1] = y.y;
+      }
 #pragma unroll
-      for (int i = 0; i < E; ++i) acc[i] += wk * src[i];
+      for (int i = 0; i < E; ++i) acc[i] += wk * x[i];
     }
   }
 #pragma unroll
   for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, d);
-  const bool none = sum == 0.0f;
-  const float inv = none ? 0.0f : 1.0f / sum;
+  if (lane == 0) {
+    s_top[warp] = top;
+    s_sum[warp] = sum;
+  }
+#pragma unroll
+  for (int i = 0; i < E; ++i) s_acc[warp][lane * E + i] = acc[i];
+  __syncthreads();
+  const float mx = fmaxf(fmaxf(s_top[0], s_top[1]), fmaxf(s_top[2], s_top[3])), ms = mx == -INFINITY ? 0.0f : mx;
+  float total = 0.0f, out = 0.0f;
+#pragma unroll
+  for (int w = 0; w < 4; ++w) {
+    const float f = ex2(s_top[w] - ms);
+    total += s_sum[w] * f;
+    if (tid < D) out += s_acc[w][tid] * f;
+  }
   const int group = p.Hq / p.Hkv, rr = cut.row + r;
   const int64_t at = (int64_t)(rr / group) * p.Hq + cut.head * group + rr % group;
-#pragma unroll
-  for (int i = 0; i < E; ++i) p.out[at * D + lane * E + i] = __float2bfloat16(none ? 0.0f : acc[i] * inv);
-  if (p.lse != nullptr && lane == 0) p.lse[at] = none ? -INFINITY : (top + log2f(sum)) * 0.6931471805599453f;
+  if (tid < D) p.out[at * D + tid] = __float2bfloat16(total == 0.0f ? 0.0f : out / total);
+  if (p.lse != nullptr && tid == 0)
+    p.lse[at] = total == 0.0f ? -INFINITY : (mx + log2f(total)) * 0.6931471805599453f;
 }
 
 template <int D, int NT>
@@ -691,18 +736,24 @@ size_t carve(Params* p, void* base) {
 template <int D, int NT>
 cudaError_t launch(const KvAttention& a, cudaStream_t st) {
   using G = Geo<D, NT>;
-  Params p = {static_cast<const __nv_bfloat16*>(a.q), a.k_codes, a.k_exps, a.v_codes, a.v_exps, a.table, a.kv_lens,
+  Params p = {static_cast<const __nv_bfloat16*>(a.q), a.k_exps, a.v_exps, a.table, a.kv_lens,
               a.query_start, static_cast<__nv_bfloat16*>(a.out), a.lse, a.dev_status, nullptr, nullptr, nullptr,
               nullptr, a.ld_q, a.ld_table, a.num_pages, a.M, a.T, a.B, a.Hq, a.Hkv, kv::log2_page(a.page_size),
               a.scale};
   carve<D, NT>(&p, a.workspace);
+  CUtensorMap tm_k, tm_v;
+  const uint32_t box = a.page_size < kTile ? a.page_size : kTile;
+  const uint64_t blocks = (uint64_t)a.num_pages * a.Hkv;
+  if (make_tmap_3d_u8(&tm_k, a.k_codes, D, a.page_size, blocks, box, D) != cudaSuccess ||
+      make_tmap_3d_u8(&tm_v, a.v_codes, D, a.page_size, blocks, box, D) != cudaSuccess)
+    return cudaErrorInvalidValue;
   cudaError_t e = ensure_dynamic_smem(reinterpret_cast<const void*>(kv_attention_kernel<D, NT>), G::SMEM_BYTES);
   if (e != cudaSuccess) return e;
   const int ctas = num_sms() * G::CTAS;
-  e = launch_pdl(kv_attention_kernel<D, NT>, ctas, G::THREADS, G::SMEM_BYTES, st, p);
+  e = launch_pdl(kv_attention_kernel<D, NT>, ctas, G::THREADS, G::SMEM_BYTES, st, tm_k, tm_v, p);
   // a table that holds no sequence long enough to be split needs no join
   if (e != cudaSuccess || (int64_t)a.M * a.page_size <= kWholeKeys) return e;
-  return launch_pdl(kv_attention_join_kernel<D, NT>, dim3(ctas - 1, G::ROWS / 4), 128, 0, st, p, ctas);
+  return launch_pdl(kv_attention_join_kernel<D, NT>, dim3(ctas - 1, G::ROWS), 128, 0, st, p, ctas);
 }
 
 }  // namespace

@@ -57,4 +57,20 @@ cudaError_t make_tmap_2d_f32(CUtensorMap* map, const void* base, uint64_t inner,
   return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
+cudaError_t make_tmap_3d_u8(CUtensorMap* map, const void* base, uint64_t inner, uint64_t rows, uint64_t blocks,
+                            uint32_t box_rows, int swizzle_bytes) {
+  PFN_cuTensorMapEncodeTiled_v12000 fn = encode_fn();
+  if (fn == nullptr) return cudaErrorNotSupported;
+  if (inner == 0 || rows == 0 || blocks == 0) return cudaErrorInvalidValue;
+  cuuint64_t dims[3] = {inner, rows, blocks};
+  cuuint64_t strides[2] = {inner, inner * rows};
+  cuuint32_t box[3] = {(cuuint32_t)inner, box_rows, 1};
+  cuuint32_t estr[3] = {1, 1, 1};
+  CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(base), dims, strides, box, estr,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE,
+                  swizzle_bytes == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
 }  // namespace nvfp4moe

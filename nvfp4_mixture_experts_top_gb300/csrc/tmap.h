@@ -20,4 +20,9 @@ cudaError_t make_tmap_2d_u8(CUtensorMap* map, const void* base, uint64_t inner, 
 cudaError_t make_tmap_2d_f32(CUtensorMap* map, const void* base, uint64_t inner, uint64_t rows, uint64_t pitch_bytes,
                              uint32_t box_inner, uint32_t box_rows);
 
+// Contiguous bytes [blocks, rows, inner] with a box of box_rows whole rows of one
+// block (inner = swizzle_bytes: 64 or 128).
+cudaError_t make_tmap_3d_u8(CUtensorMap* map, const void* base, uint64_t inner, uint64_t rows, uint64_t blocks,
+                            uint32_t box_rows, int swizzle_bytes);
+
 }  // namespace nvfp4moe

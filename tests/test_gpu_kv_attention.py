@@ -273,6 +273,24 @@ def test_past_32_bit_offsets():
         _check((q, *small[0], *small[1], table, kv, [0, new]))
 
 
+@pytest.mark.parametrize("ctx,new,Hq,Hkv,D,S", [
+    ([3000 + 137 * i for i in range(24)], [1] * 24, 16, 8, 128, 64),
+    ([70000, 300, 41000], [1, 1, 1], 8, 8, 128, 16),
+    ([2000 + 311 * i for i in range(20)], [1 + i % 3 for i in range(20)], 24, 8, 64, 32),
+    ([2000 + 311 * i for i in range(20)], [1 + i % 3 for i in range(20)], 24, 8, 128, 128),
+])
+def test_whole_gpu_many_times_over(ctx, new, Hq, Hkv, D, S):
+    """Every CTA streams its share through its buffers many times, in calls that follow one another at once."""
+    dev = cuda_or_skip()
+    case = _case(ctx, new, Hq, Hkv, D, S, 61, dev)
+    out, lse = _check(case)
+    args = case[:6] + (_i32(case[6], dev), _i32(case[7], dev), max(new))
+    ws = torch.empty(B.kv_attention_workspace_bytes(out.shape[0], len(ctx), Hq, Hkv, D), dtype=torch.uint8, device=dev)
+    again = [B.kv_attention(*args, workspace=ws, want_lse=True) for _ in range(50)]
+    for o, z in again:
+        assert torch.equal(o, out) and torch.equal(z, lse)
+
+
 @pytest.mark.parametrize("seed", range(12))
 def test_random_mixes(seed):
     dev = cuda_or_skip()
