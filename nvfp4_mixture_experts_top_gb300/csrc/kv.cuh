@@ -17,11 +17,32 @@ __device__ __forceinline__ uint32_t encode4(float a, float b, float c, float d) 
   return (uint32_t)lo | ((uint32_t)hi << 16);
 }
 
-// Two E4M3 codes -> f16x2 (exact: every E4M3 value is an f16 value).
-__device__ __forceinline__ uint32_t decode2(uint16_t c) {
+// Four f16 values -> four E5M2 codes, and the f16 values of two of them (a code is
+// the high byte of its value).
+__device__ __forceinline__ uint32_t encode_e5m2(__half2 ab, __half2 cd) {
   uint32_t r;
-  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"(c));
+  asm("{\n\t.reg .b16 lo, hi;\n\t"
+      "cvt.rn.satfinite.e5m2x2.f16x2 lo, %1;\n\t"
+      "cvt.rn.satfinite.e5m2x2.f16x2 hi, %2;\n\t"
+      "mov.b32 %0, {lo, hi};\n\t}"
+      : "=r"(r)
+      : "r"(*reinterpret_cast<const uint32_t*>(&ab)), "r"(*reinterpret_cast<const uint32_t*>(&cd)));
   return r;
+}
+__device__ __forceinline__ __half2 e5m2_pair(uint32_t w, int pair) {
+  const uint32_t h = __byte_perm(w, 0, pair ? 0x3424 : 0x1404);
+  return *reinterpret_cast<const __half2*>(&h);
+}
+
+// Four E4M3 codes -> two f16x2 (exact: every E4M3 value is an f16 value), of the
+// low and the high two codes.
+__device__ __forceinline__ void decode4(uint32_t w, uint32_t& lo, uint32_t& hi) {
+  asm("{\n\t.reg .b16 a, b;\n\t"
+      "mov.b32 {a, b}, %2;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %0, a;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
+      : "=r"(lo), "=r"(hi)
+      : "r"(w));
 }
 
 __device__ __forceinline__ float2 f16x2_to_f32(uint32_t h) {
@@ -32,18 +53,56 @@ __device__ __forceinline__ float2 f16x2_to_f32(uint32_t h) {
 // product of an E4M3 value and 2^n is exact down to 2^-149, far below half of
 // E4M3's smallest step).
 __device__ __forceinline__ uint32_t rescale_codes(uint32_t w, float f) {
-  const float2 a = f16x2_to_f32(decode2((uint16_t)w)), b = f16x2_to_f32(decode2((uint16_t)(w >> 16)));
+  uint32_t lo, hi;
+  decode4(w, lo, hi);
+  const float2 a = f16x2_to_f32(lo), b = f16x2_to_f32(hi);
   return encode4(a.x * f, a.y * f, b.x * f, b.y * f);
 }
 
-// TMA load of a 3-D box by one elected lane of a converged warp.
-__device__ __forceinline__ void ew_tma_load_3d(void* smem_dst, const void* tmap, uint64_t* bar, int32_t x, int32_t y,
-                                               int32_t z) {
+// TMA load of a 3-D box, issued by the calling thread.
+__device__ __forceinline__ void tma_load_3d(void* smem_dst, const void* tmap, uint64_t* bar, int32_t x, int32_t y,
+                                            int32_t z) {
   asm volatile(
-      "{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t"
-      "@e cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-      " [%0], [%1, {%2, %3, %4}], [%5];\n\t}" ::"r"(smem_u32(smem_dst)),
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(smem_u32(smem_dst)),
       "l"(tmap), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar))
+      : "memory");
+}
+
+// Byte offset of 16-byte chunk c of row r in rows of D bytes, as the TMA's swizzle
+// of D bytes (128 or 64) places it.
+template <int D>
+__device__ __forceinline__ uint32_t swizzled(int r, int c) {
+  return D == 128 ? r * 128 + ((c ^ (r & 7)) << 4) : r * 64 + ((c ^ (r >> 1 & 3)) << 4);
+}
+
+// D[tmem] (+)= A[smem] * B[smem], E4M3 operands, fp32 accumulation (M = 128, K = 32).
+__device__ __forceinline__ void ew_mma_e4m3(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                            uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, e;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "elect.sync _|e, 0xffffffff;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+// Warp-collective TMEM load and store: 32 lanes x 16 consecutive 32-bit columns.
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+      "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
       : "memory");
 }
 

@@ -1,0 +1,437 @@
+// kv_attention.cuh -- what the attention kernels over the 8-bit cache share: their
+// parameters, the division of the work, the page look-ups and copies, and the kernel
+// that joins what was cut.
+#pragma once
+
+#include <cuda.h>
+
+#include "common.cuh"
+#include "kernels.h"
+#include "kv.cuh"
+#include "tmap.h"
+
+namespace nvfp4moe {
+namespace kv {
+
+constexpr int kTile = 128;       // keys of a step
+constexpr int kWholeKeys = 512;  // if no sequence is longer, none is cut
+constexpr int kHeads = 8;        // tile headers in flight
+constexpr int kPieceCost = 3;    // what a sequence costs besides its tiles, in tiles
+constexpr int kThreads = 192;    // warps 0-3 softmax, 4 copies, 5 products
+constexpr float kSlack = 2.0f;   // log2 by which a logit may pass the reference
+constexpr float kBoost = 13.5f;  // log2 of the weights' shift: 2^(13.5 + 2) is in the range of E5M2 and f16
+constexpr int kNoPage = -1000;   // value exponent of keys that have no page
+constexpr int kFarExp = -60;     // value blocks further below the largest one count as this far
+
+// The sequence that a CTA's range starts in, for the join: its work before the
+// range and in all, its first output row (token * group + head in group), K/V
+// head and rows.
+struct Cut {
+  int32_t before, span, row, head, rows, pad[3];
+};
+// The work of the whole call, and the CTAs that share it (0: nothing is cut).
+struct Total {
+  int64_t work;
+  int32_t ctas;
+};
+
+struct Params {
+  const __nv_bfloat16* q;
+  const uint8_t *k_exps, *v_exps;
+  const int32_t *table, *kv_lens, *query_start;
+  __nv_bfloat16* out;
+  float* lse;
+  int32_t* dev_status;
+  Total* total;
+  Cut* cut;         // [CTA]
+  float* part;      // [CTA][2][rows][D] outputs of a CTA's first and last sequence
+  float* part_lse;  // [CTA][2][rows] their log2-sums
+  int64_t ld_q, ld_table, num_pages;
+  int M, T, B, Hq, Hkv, shift;
+  float scale;
+};
+
+// A request as the kernel sees it: lengths cut to what the table, q and out hold.
+struct Request {
+  int q0, n, kv;
+  bool bad;
+};
+__device__ __forceinline__ Request get_request(const Params& p, int b) {
+  Request r;
+  const int a = p.query_start[b], e = p.query_start[b + 1], kv = p.kv_lens[b];
+  r.q0 = min(max(a, 0), p.T);
+  const int q1 = min(max(e, r.q0), p.T);
+  r.n = q1 - r.q0;
+  const int64_t cap = (int64_t)p.M << p.shift;
+  r.kv = kv < 0 ? 0 : (kv > cap ? (int)cap : kv);
+  r.bad = r.q0 != a || q1 != e || r.kv != kv;
+  return r;
+}
+__device__ __forceinline__ float reciprocal(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float lg2(float x) {
+  float y;
+  asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// Inclusive sum over the lanes.
+__device__ __forceinline__ int64_t warp_scan(int64_t v, int lane) {
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const int64_t a = __shfl_up_sync(0xFFFFFFFFu, v, d);
+    if (lane >= d) v += a;
+  }
+  return v;
+}
+
+__device__ __forceinline__ int64_t divide(int64_t a, int64_t b) {
+  return (a | b) >> 32 ? a / b : (int64_t)((uint32_t)a / (uint32_t)b);  // (a 64-bit division takes a few times as long)
+}
+
+// n items in equal shares of parts, the first ones one item larger.
+struct Shares {
+  int64_t q, r;
+  __device__ __forceinline__ Shares(int64_t n, int parts) : q(divide(n, parts)), r(n - q * parts) {}
+  __device__ __forceinline__ int64_t start(int c) const { return q * c + min((int64_t)c, r); }
+  __device__ __forceinline__ int owner(int64_t u) const {
+    return (int)(u < r * (q + 1) ? divide(u, q + 1) : r + divide(u - r * (q + 1), q));
+  }
+};
+
+// Walks the pieces of sequences that a range of the work consists of.  A sequence
+// counts kPieceCost and its tiles; a cut inside the cost falls before its first
+// tile.
+template <int R>
+struct Pieces {
+  int b;         // request
+  int64_t off;   // work of the request before the position
+  int64_t left;  // work of the range after the position
+  // the current piece
+  Request rq;
+  int hk, row0, nrows, span, u0, take;
+  int limit;     // keys that the last row of the tile sees
+  int t0, nt;    // its tiles (fewer than it counts where the rows see fewer keys)
+
+  __device__ __forceinline__ static int span_of(int kv) {
+    return kPieceCost + (kv > kTile ? (kv - 1) / kTile + 1 : 1);
+  }
+  __device__ __forceinline__ static int row_tiles(int n, int group) { return (n * group + R - 1) / R; }
+  __device__ __forceinline__ bool next(const Params& p, int group) {
+    if (left <= 0) return false;
+    int tiles;
+    for (;; ++b) {
+      if (b >= p.B) return false;
+      rq = get_request(p, b);
+      span = span_of(rq.kv);
+      tiles = row_tiles(rq.n, group);
+      const int64_t w = (int64_t)tiles * p.Hkv * span;
+      if (off < w) break;
+      off -= w;
+    }
+    const int seq = (int)divide(off, span);
+    u0 = (int)(off - (int64_t)seq * span);
+    take = (int)min((int64_t)(span - u0), left);
+    hk = tiles == 1 ? seq : seq / tiles;
+    row0 = (seq - hk * tiles) * R;
+    nrows = min(R, rq.n * group - row0);
+    limit = rq.n == 1 ? rq.kv : min(rq.kv, rq.kv - rq.n + (row0 + nrows - 1) / group + 1);
+    t0 = max(u0 - kPieceCost, 0);
+    nt = max(min(u0 + take - kPieceCost, limit > 0 ? (limit - 1) / kTile + 1 : 0) - t0, 0);
+    off += take;
+    left -= take;
+    return true;
+  }
+};
+
+struct RangeScratch {
+  int64_t sum[2][kThreads / 32], off;
+  int longest[kThreads / 32], b;
+};
+
+// The CTA's range: of the work if some sequence is longer than kWholeKeys, else of
+// whole sequences.  (The whole CTA; left stays 0 for a CTA that has none.)
+template <int R>
+__device__ __forceinline__ void range_of_cta(const Params& p, int group, Pieces<R>& it, RangeScratch& x) {
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  constexpr int W = kThreads / 32;
+  it.left = 0;
+  const int per = (p.B + kThreads - 1) / kThreads;
+  const int b0 = min(tid * per, p.B), b1 = min(b0 + per, p.B);
+  int64_t seqs = 0, work = 0;
+  int longest = 0;
+  bool bad = false;
+  for (int b = b0; b < b1; ++b) {
+    const Request r = get_request(p, b);
+    const int n = Pieces<R>::row_tiles(r.n, group) * p.Hkv;
+    seqs += n;
+    work += (int64_t)n * Pieces<R>::span_of(r.kv);
+    if (n) longest = max(longest, r.kv);
+    bad |= r.bad;
+  }
+  if (bad && blockIdx.x == 0) report_status(p.dev_status, NVFP4_E_BAD_PAGE);
+  longest = __reduce_max_sync(0xFFFFFFFFu, longest);
+  const int64_t in_w = warp_scan(work, lane), in_s = warp_scan(seqs, lane);
+  if (lane == 31) {
+    x.sum[0][warp] = in_s;
+    x.sum[1][warp] = in_w;
+    x.longest[warp] = longest;
+  }
+  __syncthreads();
+  #pragma unroll
+  for (int w = 0; w < W; ++w) longest = max(longest, x.longest[w]);
+  const bool split = longest > kWholeKeys;
+  int64_t total = 0, all = 0, before = split ? in_w - work : in_s - seqs;
+#pragma unroll
+  for (int w = 0; w < W; ++w) {
+    const int64_t n = x.sum[split ? 1 : 0][w];
+    total += n;
+    all += x.sum[1][w];
+    if (w < warp) before += n;
+  }
+  const int ctas = (int)min(total, (int64_t)gridDim.x), c = blockIdx.x;
+  if (c == 0 && tid == 0) *p.total = {all, split ? ctas : 0};
+  if (c < ctas) {
+    const Shares sh(total, ctas);
+    const int64_t lo = sh.start(c), n = sh.start(c + 1) - lo;
+    if (before <= lo && lo < before + (split ? work : seqs)) {
+      for (int b = b0; b < b1; ++b) {
+        const Request r = get_request(p, b);
+        const int span = Pieces<R>::span_of(r.kv);
+        const int64_t seqs_b = (int64_t)Pieces<R>::row_tiles(r.n, group) * p.Hkv, w = split ? seqs_b * span : seqs_b;
+        if (lo < before + w) {
+          x.b = b;
+          x.off = split ? lo - before : (lo - before) * span;
+          break;
+        }
+        before += w;
+      }
+    }
+    __syncthreads();
+    it.b = x.b;
+    it.off = x.off;
+    it.left = n;
+    if (!split) {  // sequences to work
+      int64_t rest = n, skip = -1;
+      it.left = 0;
+      for (int b = it.b; b < p.B && rest > 0; ++b) {
+        const Request r = get_request(p, b);
+        const int span = Pieces<R>::span_of(r.kv);
+        if (skip < 0) skip = divide(it.off, span);
+        const int64_t k = min(rest, (int64_t)Pieces<R>::row_tiles(r.n, group) * p.Hkv - skip);
+        skip = 0;
+        it.left += k * span;
+        rest -= k;
+      }
+    }
+  }
+}
+
+// What the copying warp says of a tile: scale and exponent of its pages, and the
+// smallest (kNoPage: some page is missing) and largest exponent.
+struct Heads {
+  uint64_t full[kHeads];
+  float kscale[kHeads][8];
+  int vexp[kHeads][8];
+  int2 vrange[kHeads];
+};
+
+// The copying warp: K and V of the range's tiles in turn through a ring of SUBS
+// slots of kTile * D bytes, page by page.
+template <int D, int SUBS, int R>
+__device__ __forceinline__ void copy_tiles(const Params& p, int group, Pieces<R>& it, const CUtensorMap* tm_k,
+                                           const CUtensorMap* tm_v, uint8_t* ring, uint64_t* full, uint64_t* empty,
+                                           Heads& heads, volatile int* abort_flag) {
+  const int lane = threadIdx.x & 31;
+  bool ok = true;
+  int gc = 0;
+  const int pp = 7 - p.shift, per_tile = 1 << pp;  // pages of a tile
+  const uint32_t page_bytes = (uint32_t)D << p.shift;
+  int sub = 0;
+  uint32_t phase = 1, issued = 0, issued_par = 0;
+  while (ok && it.next(p, group)) {
+    const int32_t* table = p.table + it.b * p.ld_table;
+    int page = -1, ve = kNoPage;  // a page per lane, 32 >> pp tiles at a time
+    float ks = 0.0f;
+    const int t1 = it.t0 + it.nt;
+    for (int tile = it.t0; tile < t1; ++tile, ++gc) {
+      const int j = ((tile - it.t0) << pp) & 31;
+      if (j == 0) {
+        page = -1;
+        ve = kNoPage;
+        ks = 0.0f;
+        const int first = tile << pp;  // page of the sequence
+        if (((int64_t)(first + lane) << p.shift) < it.limit && first + lane < t1 << pp) {
+          page = table[first + lane];
+          if (page < 0 || page >= p.num_pages) {
+            page = -1;
+            report_status(p.dev_status, NVFP4_E_BAD_PAGE);
+          } else {
+            const int64_t at = (int64_t)page * p.Hkv + it.hk;
+            ks = exp2_int(p.k_exps[at] - 127);
+            ve = p.v_exps[at] - 127;
+          }
+        }
+        __syncwarp();
+      }
+      const bool mine = lane >= j && lane < j + per_tile;
+      const uint32_t here = __popc(__ballot_sync(0xFFFFFFFFu, mine && page >= 0)) * page_bytes;
+      for (int h = 0; h < 2 && ok; ++h) {
+        if (!warp_wait(&empty[sub], phase, abort_flag, p.dev_status)) {
+          ok = false;
+          break;
+        }
+        ew_arrive_expect_tx(&full[sub], here);
+        __syncwarp();
+        if (mine && page >= 0)
+          tma_load_3d(ring + sub * kTile * D + (lane - j) * page_bytes, h ? tm_v : tm_k, &full[sub], 0, 0,
+                          page * p.Hkv + it.hk);
+        __syncwarp();
+        issued |= 1u << sub;
+        issued_par = (issued_par & ~(1u << sub)) | ((phase ^ 1) << sub);
+        if (++sub == SUBS) {
+          sub = 0;
+          phase ^= 1;
+        }
+      }
+      if (!ok) break;
+      // the tile's scales and exponents arrive later than the page ids
+      if (mine) {
+        heads.kscale[gc & (kHeads - 1)][lane - j] = ks;
+        heads.vexp[gc & (kHeads - 1)][lane - j] = ve;
+      }
+      const bool used = mine && tile * kTile + ((lane - j) << p.shift) < it.limit;
+      const int vmin = __reduce_min_sync(0xFFFFFFFFu, used ? ve : 1000);
+      const int vmax = __reduce_max_sync(0xFFFFFFFFu, used ? ve : kNoPage);
+      if (lane == 0) heads.vrange[gc & (kHeads - 1)] = make_int2(vmin, vmax);
+      __syncwarp();
+      ew_arrive(&heads.full[gc & (kHeads - 1)]);
+    }
+  }
+  if (!ok) {  // given up: no copy may outlive the CTA's memory
+    for (int i = 0; i < SUBS; ++i)
+      if (issued >> i & 1) mbar_wait(&full[i], issued_par >> i & 1);
+  }
+}
+
+// Joins the partial results of a sequence that was cut by CTAs: CTA c - 1 takes
+// the one that the range of CTA c of the attention starts in, if no range before
+// c starts inside it.  A warp per row, parts in order.
+template <int D, int R>
+__global__ void __launch_bounds__(256) kv_attention_join_kernel(const Params p) {
+  constexpr int E = D / 32;
+  pdl_wait();
+  pdl_trigger();
+  const int c = blockIdx.x + 1, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const Total all = *p.total;
+  const Cut cut = p.cut[c];
+  if (c >= all.ctas || cut.before == 0) return;
+  const Shares sh(all.work, all.ctas);
+  const int64_t a = sh.start(c) - cut.before;
+  const int c0 = sh.owner(a);
+  if (sh.owner(a + cut.before - 1) != c0) return;
+  // a part per CTA: part 0 of the sequence that its range starts in, else part 1
+  const int n = sh.owner(a + cut.span - 1) - c0 + 1;
+  const int first = c0 * 2 + (sh.start(c0) >= a ? 0 : 1);
+  for (int r = warp; r < cut.rows; r += 8) {
+    float top = -INFINITY, sum = 0.0f, acc[E] = {};
+    for (int k0 = 0; k0 < n; k0 += 32) {
+      const int m = min(32, n - k0), k = k0 + min(lane, m - 1);
+      const int row = (k == 0 ? first : (c0 + k) * 2) * R + r;
+      const float z = lane < m ? p.part_lse[row] : -INFINITY;
+      float mx = z;
+#pragma unroll
+      for (int d = 16; d > 0; d >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, d));
+      const float t1 = fmaxf(top, mx), ms = t1 == -INFINITY ? 0.0f : t1, f = ex2(top - ms), w = ex2(z - ms);
+      top = t1;
+      sum = sum * f + w;
+#pragma unroll
+      for (int i = 0; i < E; ++i) acc[i] *= f;
+#pragma unroll 16
+      for (int i = 0; i < m; ++i) {
+        const float wi = __shfl_sync(0xFFFFFFFFu, w, i);
+        const float* src = p.part + (int64_t)__shfl_sync(0xFFFFFFFFu, row, i) * D + lane * E;
+        if constexpr (E == 4) {
+          const float4 y = *reinterpret_cast<const float4*>(src);
+          acc[0] += wi * y.x, acc[1] += wi * y.y, acc[2] += wi * y.z, acc[3] += wi * y.w;
+        } else {
+          const float2 y = *reinterpret_cast<const float2*>(src);
+          acc[0] += wi * y.x, acc[1] += wi * y.y;
+        }
+      }
+    }
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, d);
+    const bool empty = sum == 0.0f;
+    const float inv = empty ? 0.0f : reciprocal(sum);
+    const int group = p.Hq / p.Hkv, rr = cut.row + r;
+    const int64_t at = (int64_t)(rr / group) * p.Hq + cut.head * group + rr % group;
+#pragma unroll
+    for (int i = 0; i < E; i += 2) {
+      const __nv_bfloat162 x =
+          __floats2bfloat162_rn(empty ? 0.0f : acc[i] * inv, empty ? 0.0f : acc[i + 1] * inv);
+      *reinterpret_cast<__nv_bfloat162*>(p.out + at * D + lane * E + i) = x;
+    }
+    if (p.lse != nullptr && lane == 0) p.lse[at] = empty ? -INFINITY : (top + lg2(sum)) * 0.6931471805599453f;
+  }
+}
+
+// Lays out the workspace of `ctas` CTAs.
+template <int D, int R>
+size_t carve(Params* p, void* base, size_t ctas) {
+  uint8_t* b = static_cast<uint8_t*>(base);
+  size_t off = 0;
+  auto take = [&](size_t bytes) {
+    uint8_t* at = b ? b + off : nullptr;
+    off += (bytes + 255) & ~(size_t)255;
+    return at;
+  };
+  uint8_t* total = take(sizeof(Total));
+  uint8_t* cut = take(ctas * sizeof(Cut));
+  uint8_t* lse = take(ctas * 2 * R * sizeof(float));
+  uint8_t* part = take(ctas * 2 * R * D * sizeof(float));
+  if (p != nullptr) {
+    p->total = reinterpret_cast<Total*>(total);
+    p->cut = reinterpret_cast<Cut*>(cut);
+    p->part_lse = reinterpret_cast<float*>(lse);
+    p->part = reinterpret_cast<float*>(part);
+  }
+  return off;
+}
+
+// Launches `kernel` on `per_sm` CTAs per SM, and the join where something may be cut.
+template <int D, int R, typename K>
+cudaError_t launch(K kernel, int per_sm, int smem_bytes, const KvAttention& a, cudaStream_t st) {
+  Params p = {static_cast<const __nv_bfloat16*>(a.q), a.k_exps, a.v_exps, a.table, a.kv_lens, a.query_start,
+              static_cast<__nv_bfloat16*>(a.out), a.lse, a.dev_status, nullptr, nullptr, nullptr, nullptr, a.ld_q,
+              a.ld_table, a.num_pages, a.M, a.T, a.B, a.Hq, a.Hkv, log2_page(a.page_size), a.scale};
+  const int ctas = num_sms() * per_sm;
+  carve<D, R>(&p, a.workspace, ctas);
+  CUtensorMap tm_k, tm_v;  // a page of a head at a time
+  const uint64_t blocks = (uint64_t)a.num_pages * a.Hkv;
+  if (make_tmap_3d_u8(&tm_k, a.k_codes, D, a.page_size, blocks, a.page_size, D) != cudaSuccess ||
+      make_tmap_3d_u8(&tm_v, a.v_codes, D, a.page_size, blocks, a.page_size, D) != cudaSuccess)
+    return cudaErrorInvalidValue;
+  cudaError_t e = ensure_dynamic_smem(reinterpret_cast<const void*>(kernel), smem_bytes);
+  if (e != cudaSuccess) return e;
+  e = launch_pdl(kernel, ctas, kThreads, smem_bytes, st, tm_k, tm_v, p);
+  // a table that holds no sequence long enough to be cut needs no join
+  if (e != cudaSuccess || (int64_t)a.M * a.page_size <= kWholeKeys) return e;
+  return launch_pdl(kv_attention_join_kernel<D, R>, ctas - 1, 256, 0, st, p);
+}
+
+}  // namespace kv
+
+// Many query rows per K/V head and request (kv_prompt.cu).
+size_t kv_prompt_ws_bytes(int D);
+cudaError_t launch_kv_prompt(const KvAttention& a, cudaStream_t st);
+
+}  // namespace nvfp4moe

@@ -1,0 +1,390 @@
+// kv_prompt.cu -- attention over the paged 8-bit key/value cache for many query rows
+// per request and K/V head (prompt chunks): a tile of 128 rows against tiles of 128
+// keys, S = Q K^T and O += P V on tcgen05 with the cached codes as they are.
+//
+// A row is a lane: its maximum, sum and reference are a thread's own.  What meets the
+// codes is the sum of a few 8-bit terms, accumulated in place (kind::f8f6f4, fp32):
+//   q = 2^-e (q1 + q2)         E4M3: exact for what bf16 holds down to 2^-9 of the
+//                              row's largest element, within 2^-17 of it
+//   p = p1 + p2 + p3           E5M2: 9 significant bits, down to 2^-30 of the row's
+//                              largest weight
+// so a tile takes 2 + 3 products of 128 x 128 x D at twice the f16 rate, 1280 cycles
+// at D = 128, next to about 1100 of conversions (8 ALU cycles per weight on each of
+// the SM's four schedulers).  S is double buffered, so that both run at a time.
+//
+// Roles, ring, division of the work and join as in kv_attention.cu; one CTA per SM.
+#include "kv_attention.cuh"
+
+namespace nvfp4moe {
+namespace {
+
+using namespace kv;
+
+constexpr int kRows = 128;
+
+template <int D>
+struct Geo {
+  static constexpr int QOFF = 0;                            // [2 terms][128][D]
+  static constexpr int POFF = QOFF + 2 * kRows * D;         // [3 terms][128 rows][128 keys]
+  static constexpr int ROFF = POFF + 3 * kRows * kTile;
+  static constexpr int SUBS = D == 128 ? 8 : 10;
+  static constexpr int SMEM_BYTES = ROFF + SUBS * kTile * D;
+  static constexpr int OCOL = 2 * kTile;                    // TMEM: two S, then O
+  static constexpr int COLS = 512;
+};
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1)
+    kv_prompt_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
+                     const Params p) {
+  using G = Geo<D>;
+  constexpr int SUBS = G::SUBS;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  __shared__ __align__(8) uint64_t full[SUBS], empty[SUBS], s_full[2], s_empty[2], q_full, p_full, pv_done, drained;
+  __shared__ Heads heads;
+  __shared__ RangeScratch scratch;
+  __shared__ uint32_t tmem_s;
+  __shared__ volatile int abort_flag;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int group = p.Hq / p.Hkv;
+  if (tid == 0) {
+    for (int i = 0; i < SUBS; ++i) {
+      mbar_init(&full[i], 1);
+      mbar_init(&empty[i], 1);
+    }
+    for (int i = 0; i < kHeads; ++i) mbar_init(&heads.full[i], 1);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&s_full[i], 1);
+      mbar_init(&s_empty[i], 4);
+    }
+    mbar_init(&q_full, 4);
+    mbar_init(&p_full, 4);
+    mbar_init(&pv_done, 1);
+    mbar_init(&drained, 1);
+    abort_flag = 0;
+    fence_mbar_init();
+    prefetch_tmap(&tm_k);
+    prefetch_tmap(&tm_v);
+  }
+  if (warp == 5) {
+    tmem_alloc(&tmem_s, G::COLS);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  pdl_wait();
+  pdl_trigger();  // after this CTA's TMEM allocation
+  const uint32_t tmem = tmem_s;
+  Pieces<kRows> it;
+  range_of_cta<kRows>(p, group, it, scratch);
+
+  bool ok = true;
+  int gc = 0;  // tiles of the CTA so far, the same count in every role
+  auto wait = [&](uint64_t* bar, uint32_t parity) {
+    // (after a failure the softmax warps go on without waiting)
+    if (ok) ok = warp_wait(bar, parity, &abort_flag, p.dev_status);
+    return ok;
+  };
+  if (warp == 4) {
+    copy_tiles<D, SUBS, kRows>(p, group, it, &tm_k, &tm_v, smem + G::ROFF, full, empty, heads, &abort_flag);
+  } else if (warp == 5) {
+    // ------------------------------------------------------------ products
+    // A = P is E5M2 (bit 7), B = V is MN-major (bit 16)
+    constexpr uint32_t idesc_s = idesc_e4m3(kRows, kTile, false);
+    constexpr uint32_t idesc_o = idesc_e4m3(kRows, D, false) | (1u << 7) | (1u << 16);
+    constexpr uint32_t layout = D == 128 ? 2 : 4;  // swizzle of rows of D bytes
+    const uint32_t base = smem_u32(smem), ring = base + G::ROFF;
+    int sub = 0;
+    uint32_t phase = 0, q_phase = 0;
+    bool issued = false;
+    auto advance = [&] {
+      if (++sub == SUBS) {
+        sub = 0;
+        phase ^= 1;
+      }
+    };
+    auto product_s = [&](int n) {  // S of tile n of the CTA: K's slot is the current one
+      if (!wait(&full[sub], phase) || !wait(&s_empty[n & 1], ((n >> 1) & 1) ^ 1)) return;
+      tc_fence_after();
+#pragma unroll
+      for (int t = 0; t < 2; ++t)
+#pragma unroll
+        for (int k = 0; k < D / 32; ++k)
+          ew_mma_e4m3(tmem + (n & 1) * kTile, smem_desc(base + G::QOFF + t * kRows * D + k * 32, 16, 8 * D, layout),
+                      smem_desc(ring + sub * kTile * D + k * 32, 16, 8 * D, layout), idesc_s, t > 0 || k > 0);
+      ew_commit(&empty[sub]);
+      ew_commit(&s_full[n & 1]);
+      issued = true;
+    };
+    while (ok && it.next(p, group)) {
+      const int nt = it.nt;
+      if (nt == 0) continue;
+      if (!wait(&q_full, q_phase)) break;
+      q_phase ^= 1;
+      product_s(gc);
+      for (int i = 0; i < nt && ok; ++i, ++gc) {
+        advance();  // to V of this tile
+        const int v_sub = sub;
+        const uint32_t v_phase = phase;
+        advance();
+        if (i + 1 < nt) product_s(gc + 1);
+        if (!wait(&full[v_sub], v_phase) || !wait(&heads.full[gc & (kHeads - 1)], gc / kHeads & 1)) break;
+        // rows past the sequence hold anything, and 0 * NaN would spread: zeros instead
+        const int key0 = (it.t0 + i) * kTile;
+        if (key0 + kTile > it.limit || heads.vrange[gc & (kHeads - 1)].x == kNoPage) {
+          for (int r = lane; r < kTile; r += 32)
+            if (key0 + r >= it.limit || heads.vexp[gc & (kHeads - 1)][r >> p.shift] == kNoPage) {
+#pragma unroll
+              for (int c = 0; c < D / 16; ++c)
+                *reinterpret_cast<uint4*>(smem + G::ROFF + v_sub * kTile * D + r * D + c * 16) =
+                    make_uint4(0, 0, 0, 0);
+            }
+          fence_proxy_async_smem();
+          __syncwarp();
+        }
+        if (!wait(&p_full, gc & 1)) break;
+        tc_fence_after();
+#pragma unroll
+        for (int t = 0; t < 3; ++t)
+#pragma unroll
+          for (int k = 0; k < kTile / 32; ++k)
+            ew_mma_e4m3(tmem + G::OCOL, smem_desc(base + G::POFF + t * kRows * kTile + k * 32, 16, 1024, 2),
+                        smem_desc(ring + v_sub * kTile * D + k * 32 * D, 0, 8 * D, layout),
+                        idesc_o, i > 0 || t > 0 || k > 0);
+        ew_commit(&empty[v_sub]);
+        ew_commit(&pv_done);
+      }
+    }
+    if (!ok && issued) {  // given up: no product may outlive the operands and the TMEM
+      ew_commit(&drained);
+      mbar_wait(&drained, 0);
+    }
+  } else {
+    // ------------------------------------------------------------ softmax, a row per thread
+    const uint32_t lane_tmem = tmem + ((uint32_t)(warp * 32) << 16);
+    bool first = true;
+    while (it.next(p, group)) {
+      const int nt = it.nt, rr = it.row0 + tid, tok = rr / group;
+      const bool live = tid < it.nrows;
+      const int64_t at = (int64_t)(it.rq.q0 + tok) * p.Hq + it.hk * group + rr - tok * group;
+      if (first && tid == 0)
+        p.cut[blockIdx.x] = {it.u0, it.span, it.rq.q0 * group + it.row0, it.hk, it.nrows, {0, 0, 0}};
+      // keys that the row sees; that all of the tile's rows see
+      const int lim = live ? min(it.rq.kv, it.rq.kv - it.rq.n + tok + 1) : 0;
+      const int all_see = it.rq.kv - it.rq.n + it.row0 / group + 1;
+      // the row as 2^-e (q1 + q2), in the sign of the scale; not finite: a row of NaN
+      float qs = 0.0f;
+      if (nt > 0) {
+        const uint4* src = reinterpret_cast<const uint4*>(p.q + (int64_t)(it.rq.q0 + tok) * p.ld_q +
+                                                          (int64_t)(it.hk * group + rr - tok * group) * D);
+        uint4 w[D / 8];
+        float amax = 0.0f;
+#pragma unroll
+        for (int i = 0; i < D / 8; ++i) {
+          w[i] = live ? src[i] : make_uint4(0, 0, 0, 0);
+          const uint32_t x[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            amax = fmaxf(amax, fmaxf(fabsf(__uint_as_float(x[k] << 16)), fabsf(__uint_as_float(x[k] & 0xFFFF0000u))));
+        }
+        const int e = amax == 0.0f ? 0 : min(7 - floor_log2(amax), 126);
+        float f = exp2_int(e);
+        if (p.scale < 0.0f) f = -f;
+        if (!(amax <= 3.402823466e38f)) f = __int_as_float(0x7FFFFFFF);
+        // (a zero scale stays apart from a key that is not seen: -inf * qs)
+        qs = fmaxf(fabsf(p.scale) * 1.4426950408889634f * exp2_int(-e), 1.175494351e-38f);
+#pragma unroll
+        for (int c = 0; c < D / 16; ++c) {
+          uint32_t hi[4], lo[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const uint4 v = w[2 * c + (i >> 1)];
+            const uint32_t a = i & 1 ? v.z : v.x, b = i & 1 ? v.w : v.y;
+            const float x0 = __uint_as_float(a << 16) * f, x1 = __uint_as_float(a & 0xFFFF0000u) * f;
+            const float x2 = __uint_as_float(b << 16) * f, x3 = __uint_as_float(b & 0xFFFF0000u) * f;
+            hi[i] = encode4(x0, x1, x2, x3);
+            uint32_t d0, d1;
+            decode4(hi[i], d0, d1);
+            const float2 y0 = f16x2_to_f32(d0), y1 = f16x2_to_f32(d1);
+            lo[i] = encode4(x0 - y0.x, x1 - y0.y, x2 - y1.x, x3 - y1.y);
+          }
+          *reinterpret_cast<uint4*>(smem + G::QOFF + swizzled<D>(tid, c)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+          *reinterpret_cast<uint4*>(smem + G::QOFF + kRows * D + swizzled<D>(tid, c)) =
+              make_uint4(lo[0], lo[1], lo[2], lo[3]);
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        ew_arrive(&q_full);
+      }
+
+      float m = -INFINITY, ref = 0.0f, l = 0.0f;  // reference (0 while there is none), sum
+      int unit = -127;  // outputs are in units of 2^unit, the largest value exponent so far
+      for (int i = 0; i < nt; ++i, ++gc) {
+        const int key0 = (it.t0 + i) * kTile, buf = gc & 1, hd = gc & (kHeads - 1);
+        wait(&s_full[buf], (gc >> 1) & 1);
+        tc_fence_after();
+        float s[kTile];
+#pragma unroll
+        for (int c = 0; c < kTile; c += 32) {
+          uint32_t x[32];
+          tmem_ld_32x32b_x32(lane_tmem + buf * kTile + c, x);
+          tmem_ld_wait();
+#pragma unroll
+          for (int j = 0; j < 32; ++j) s[c + j] = __uint_as_float(x[j]);
+        }
+        tc_fence_before();
+        __syncwarp();
+        ew_arrive(&s_empty[buf]);
+        wait(&heads.full[hd], gc / kHeads & 1);
+        const int2 vr = heads.vrange[hd];
+        if (key0 + kTile > all_see || vr.x == kNoPage) {
+          const int seen = lim - key0;
+#pragma unroll
+          for (int j = 0; j < kTile; ++j)
+            if (j >= seen || heads.vexp[hd][j >> p.shift] == kNoPage) s[j] = -INFINITY;
+        }
+        // log2 units: s * qs * the page's scale, 16 keys at a time
+        float c[8], top = -INFINITY;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          c[k] = fminf(fmaxf(qs * heads.kscale[hd][k * 16 >> p.shift], 1.175494351e-38f), 3.402823466e38f);
+          float mx = s[16 * k];
+#pragma unroll
+          for (int j = 1; j < 16; ++j) mx = fmaxf(mx, s[16 * k + j]);
+          top = fmaxf(top, mx * c[k]);
+        }
+        const int unit1 = max(unit, vr.y);
+        if (__any_sync(0xFFFFFFFFu, top > ref + kSlack || (m == -INFINITY && top != -INFINITY)) || unit1 != unit) {
+          // the references move to the maxima, sums and outputs with them
+          const float m1 = fmaxf(m, top), r1 = m1 == -INFINITY ? 0.0f : m1, f = ex2(m - r1);
+          l *= f;
+          m = m1;
+          ref = r1;
+          if (i > 0) {
+            const float fo = f * exp2_int(max(unit - unit1, -127));
+            wait(&pv_done, (gc & 1) ^ 1);
+            tc_fence_after();
+#pragma unroll 1
+            for (int o = 0; o < D; o += 32) {
+              uint32_t x[32];
+              tmem_ld_32x32b_x32(lane_tmem + G::OCOL + o, x);
+              tmem_ld_wait();
+#pragma unroll
+              for (int j = 0; j < 32; ++j) x[j] = __float_as_uint(__uint_as_float(x[j]) * fo);
+              tmem_st_32x32b_x32(lane_tmem + G::OCOL + o, x);
+            }
+            tmem_st_wait();
+            tc_fence_before();
+          }
+          unit = unit1;
+        }
+        const float up = kBoost - ref;
+        float sum[4] = {};
+#pragma unroll
+        for (int j = 0; j < kTile; ++j) {
+          s[j] = ex2(fmaf(s[j], c[j / 16], up));
+          sum[j & 3] += s[j];
+        }
+        l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+        if (vr.x != unit) {  // (some block of the tile is below the largest)
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            const float vf = exp2_int(max(heads.vexp[hd][k * 16 >> p.shift] - unit, kFarExp));
+#pragma unroll
+            for (int j = 0; j < 16; ++j) s[16 * k + j] *= vf;
+          }
+        }
+        wait(&pv_done, (gc & 1) ^ 1);  // the last product has read P
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          uint32_t w1[4], w2[4], w3[4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const float* x = s + 16 * k + 4 * j;
+            __half2 a = __floats2half2_rn(x[0], x[1]), b = __floats2half2_rn(x[2], x[3]);
+            w1[j] = encode_e5m2(a, b);
+            a = __hsub2(a, e5m2_pair(w1[j], 0));
+            b = __hsub2(b, e5m2_pair(w1[j], 1));
+            w2[j] = encode_e5m2(a, b);
+            w3[j] = encode_e5m2(__hsub2(a, e5m2_pair(w2[j], 0)), __hsub2(b, e5m2_pair(w2[j], 1)));
+          }
+          uint8_t* dst = smem + G::POFF + swizzled<128>(tid, k);
+          *reinterpret_cast<uint4*>(dst) = make_uint4(w1[0], w1[1], w1[2], w1[3]);
+          *reinterpret_cast<uint4*>(dst + kRows * kTile) = make_uint4(w2[0], w2[1], w2[2], w2[3]);
+          *reinterpret_cast<uint4*>(dst + 2 * kRows * kTile) = make_uint4(w3[0], w3[1], w3[2], w3[3]);
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        ew_arrive(&p_full);
+      }
+
+      // ---- the piece's result
+      const bool whole = it.take == it.span, none = l == 0.0f;
+      const int64_t part = ((int64_t)blockIdx.x * 2 + (first ? 0 : 1)) * kRows + tid;
+      const float inv = none ? 0.0f : reciprocal(l), us = exp2_int(unit);
+      const float lse2 = none ? -INFINITY : ref + (lg2(l) - kBoost);
+      if (live) {
+        if (!whole) p.part_lse[part] = lse2;
+        else if (p.lse != nullptr) p.lse[at] = lse2 * 0.6931471805599453f;
+      }
+      if (nt > 0) {
+        wait(&pv_done, (gc & 1) ^ 1);
+        tc_fence_after();
+      }
+#pragma unroll 1
+      for (int o = 0; o < D; o += 32) {
+        uint32_t x[32];
+        if (nt > 0) {
+          tmem_ld_32x32b_x32(lane_tmem + G::OCOL + o, x);
+          tmem_ld_wait();
+        }
+        float y[32];
+#pragma unroll
+        for (int j = 0; j < 32; ++j) y[j] = none ? 0.0f : __uint_as_float(x[j]) * inv * us;
+        if (!live) continue;
+        if (whole) {
+          uint32_t w[16];
+#pragma unroll
+          for (int j = 0; j < 16; ++j) {
+            const __nv_bfloat162 b = __floats2bfloat162_rn(y[2 * j], y[2 * j + 1]);
+            w[j] = *reinterpret_cast<const uint32_t*>(&b);
+          }
+          uint4* dst = reinterpret_cast<uint4*>(p.out + at * D + o);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) dst[j] = make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
+        } else {
+          float4* dst = reinterpret_cast<float4*>(p.part + part * D + o);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) dst[j] = make_float4(y[4 * j], y[4 * j + 1], y[4 * j + 2], y[4 * j + 3]);
+        }
+      }
+      tc_fence_before();
+      first = false;
+    }
+    if (first && tid == 0) p.cut[blockIdx.x].before = 0;
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 5) {
+    tc_fence_after();
+    tmem_dealloc(tmem, G::COLS);
+  }
+}
+
+template <int D>
+cudaError_t launch_prompt(const KvAttention& a, cudaStream_t st) {
+  return launch<D, kRows>(kv_prompt_kernel<D>, 1, Geo<D>::SMEM_BYTES, a, st);
+}
+
+}  // namespace
+
+size_t kv_prompt_ws_bytes(int D) {
+  return D == 128 ? carve<128, kRows>(nullptr, nullptr, num_sms()) : carve<64, kRows>(nullptr, nullptr, num_sms());
+}
+
+cudaError_t launch_kv_prompt(const KvAttention& a, cudaStream_t st) {
+  return a.D == 128 ? launch_prompt<128>(a, st) : launch_prompt<64>(a, st);
+}
+
+}  // namespace nvfp4moe
