@@ -43,6 +43,9 @@ namespace {
 using namespace kv;
 
 constexpr int kCtasPerSm = 2;
+constexpr int kThreads = 192;
+constexpr float kSlack = 2.0f;   // log2 by which a logit may pass the reference
+constexpr float kBoost = 13.5f;  // log2 of the weights' shift: 2^(13.5 + 2) is in the range of E5M2 and f16
 
 // Sum of R values per lane over the warp: row_of_lane(lane)'s sum in v[0] (R a
 // power of two; each step halves the rows a lane is responsible for).
@@ -102,7 +105,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
   __shared__ __align__(8) uint64_t full[SUBS], empty[SUBS], s_full[SB], s_empty[SB], q_full, p_full,
       pv_done, drained;
   __shared__ Heads heads;
-  __shared__ RangeScratch scratch;
+  __shared__ RangeScratch<kThreads> scratch;
   __shared__ __align__(16) float2 row_qm[R];  // log2 logit per unit of S; the reference (0 where it is -inf)
   __shared__ float row_ref[R], row_fl[R], row_fo[R], wmax[4][R];
   __shared__ int row_at[R];
@@ -143,7 +146,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
   const uint32_t tmem = tmem_s;
 
   P it;
-  range_of_cta<R>(p, group, it, scratch);
+  range_of_cta<kThreads, R>(p, group, it, scratch);
 
   bool ok = true;
   int gc = 0;  // tiles of the CTA so far, the same count in every role
@@ -519,7 +522,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
 
 template <int D, int R>
 cudaError_t launch_few(const KvAttention& a, cudaStream_t st) {
-  return launch<D, R>(kv_attention_kernel<D, R>, kCtasPerSm, Geo<D, R>::SMEM_BYTES, a, st);
+  return launch<D, R>(kv_attention_kernel<D, R>, kCtasPerSm, kThreads, Geo<D, R>::SMEM_BYTES, a, st);
 }
 
 template <int D>

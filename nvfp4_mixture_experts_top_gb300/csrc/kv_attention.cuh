@@ -17,9 +17,6 @@ constexpr int kTile = 128;       // keys of a step
 constexpr int kWholeKeys = 512;  // if no sequence is longer, none is cut
 constexpr int kHeads = 8;        // tile headers in flight
 constexpr int kPieceCost = 3;    // what a sequence costs besides its tiles, in tiles
-constexpr int kThreads = 192;    // warps 0-3 softmax, 4 copies, 5 products
-constexpr float kSlack = 2.0f;   // log2 by which a logit may pass the reference
-constexpr float kBoost = 13.5f;  // log2 of the weights' shift: 2^(13.5 + 2) is in the range of E5M2 and f16
 constexpr int kNoPage = -1000;   // value exponent of keys that have no page
 constexpr int kFarExp = -60;     // value blocks further below the largest one count as this far
 
@@ -152,19 +149,20 @@ struct Pieces {
   }
 };
 
+template <int THREADS>
 struct RangeScratch {
-  int64_t sum[2][kThreads / 32], off;
-  int longest[kThreads / 32], b;
+  int64_t sum[2][THREADS / 32], off;
+  int longest[THREADS / 32], b;
 };
 
 // The CTA's range: of the work if some sequence is longer than kWholeKeys, else of
 // whole sequences.  (The whole CTA; left stays 0 for a CTA that has none.)
-template <int R>
-__device__ __forceinline__ void range_of_cta(const Params& p, int group, Pieces<R>& it, RangeScratch& x) {
+template <int THREADS, int R>
+__device__ __forceinline__ void range_of_cta(const Params& p, int group, Pieces<R>& it, RangeScratch<THREADS>& x) {
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  constexpr int W = kThreads / 32;
+  constexpr int W = THREADS / 32;
   it.left = 0;
-  const int per = (p.B + kThreads - 1) / kThreads;
+  const int per = (p.B + THREADS - 1) / THREADS;
   const int b0 = min(tid * per, p.B), b1 = min(b0 + per, p.B);
   int64_t seqs = 0, work = 0;
   int longest = 0;
@@ -186,7 +184,7 @@ __device__ __forceinline__ void range_of_cta(const Params& p, int group, Pieces<
     x.longest[warp] = longest;
   }
   __syncthreads();
-  #pragma unroll
+#pragma unroll
   for (int w = 0; w < W; ++w) longest = max(longest, x.longest[w]);
   const bool split = longest > kWholeKeys;
   int64_t total = 0, all = 0, before = split ? in_w - work : in_s - seqs;
@@ -409,7 +407,7 @@ size_t carve(Params* p, void* base, size_t ctas) {
 
 // Launches `kernel` on `per_sm` CTAs per SM, and the join where something may be cut.
 template <int D, int R, typename K>
-cudaError_t launch(K kernel, int per_sm, int smem_bytes, const KvAttention& a, cudaStream_t st) {
+cudaError_t launch(K kernel, int per_sm, int threads, int smem_bytes, const KvAttention& a, cudaStream_t st) {
   Params p = {static_cast<const __nv_bfloat16*>(a.q), a.k_exps, a.v_exps, a.table, a.kv_lens, a.query_start,
               static_cast<__nv_bfloat16*>(a.out), a.lse, a.dev_status, nullptr, nullptr, nullptr, nullptr, a.ld_q,
               a.ld_table, a.num_pages, a.M, a.T, a.B, a.Hq, a.Hkv, log2_page(a.page_size), a.scale};
@@ -422,7 +420,7 @@ cudaError_t launch(K kernel, int per_sm, int smem_bytes, const KvAttention& a, c
     return cudaErrorInvalidValue;
   cudaError_t e = ensure_dynamic_smem(reinterpret_cast<const void*>(kernel), smem_bytes);
   if (e != cudaSuccess) return e;
-  e = launch_pdl(kernel, ctas, kThreads, smem_bytes, st, tm_k, tm_v, p);
+  e = launch_pdl(kernel, ctas, threads, smem_bytes, st, tm_k, tm_v, p);
   // a table that holds no sequence long enough to be cut needs no join
   if (e != cudaSuccess || (int64_t)a.M * a.page_size <= kWholeKeys) return e;
   return launch_pdl(kv_attention_join_kernel<D, R>, ctas - 1, 256, 0, st, p);

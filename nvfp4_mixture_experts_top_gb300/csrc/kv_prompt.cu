@@ -2,17 +2,21 @@
 // per request and K/V head (prompt chunks): a tile of 128 rows against tiles of 128
 // keys, S = Q K^T and O += P V on tcgen05 with the cached codes as they are.
 //
-// A row is a lane: its maximum, sum and reference are a thread's own.  What meets the
-// codes is the sum of a few 8-bit terms, accumulated in place (kind::f8f6f4, fp32):
-//   q = 2^-e (q1 + q2)         E4M3: exact for what bf16 holds down to 2^-9 of the
-//                              row's largest element, within 2^-17 of it
-//   p = p1 + p2 + p3           E5M2: 9 significant bits, down to 2^-30 of the row's
-//                              largest weight
-// so a tile takes 2 + 3 products of 128 x 128 x D at twice the f16 rate, 1280 cycles
-// at D = 128, next to about 1100 of conversions (8 ALU cycles per weight on each of
-// the SM's four schedulers).  S is double buffered, so that both run at a time.
+// A row is a lane: its maximum, sum and reference are a thread's own.
+//   S = Q K^T   K's codes as they are (kind::f8f6f4), the query row as the sum of two
+//               E4M3 values times its power of two, 2^-e (q1 + q2): exact for what
+//               bf16 holds down to 2^-9 of the row's largest element, within 2^-17
+//   O += P V    f16: four warps widen each V tile once for all 128 rows (exact, times
+//               its block's power of two); weights have 11 bits.  Splitting weights
+//               into three 8-bit terms instead took 4.75 instructions per weight next
+//               to 0.5, and half as long again on the tensor cores: 934 us for three
+//               chunks of 1.5-2.1K tokens after 0.5-4K.
+// A tile is 512 + 512 cycles of products at D = 128, next to 512 of exponentials (a
+// quarter per cycle and scheduler); S and V's f16 form are double buffered so that
+// all run at a time.
 //
-// Roles, ring, division of the work and join as in kv_attention.cu; one CTA per SM.
+// Roles, ring, division of the work and join as in kv_attention.cu, and warps 6-9 that
+// widen V; one CTA per SM.
 #include "kv_attention.cuh"
 
 namespace nvfp4moe {
@@ -22,27 +26,35 @@ using namespace kv;
 
 constexpr int kRows = 128;
 
+constexpr int kPromptThreads = 320;
+constexpr float kRowSlack = 5.0f;   // log2 by which a logit may pass the row's reference
+constexpr float kRowBoost = 10.5f;  // log2 of the weights' shift: 2^(10.5 + 5) is in f16's range
+
 template <int D>
 struct Geo {
-  static constexpr int QOFF = 0;                            // [2 terms][128][D]
-  static constexpr int POFF = QOFF + 2 * kRows * D;         // [3 terms][128 rows][128 keys]
-  static constexpr int ROFF = POFF + 3 * kRows * kTile;
-  static constexpr int SUBS = D == 128 ? 8 : 10;
+  static constexpr int QOFF = 0;                            // [2 terms][128][D] E4M3
+  static constexpr int POFF = QOFF + 2 * kRows * D;         // [2 halves of the keys][128 rows][64] f16
+  static constexpr int VOFF = POFF + kRows * kTile * 2;     // [2 buffers][D / 64][128 keys][64] f16
+  static constexpr int ROFF = VOFF + 2 * kTile * D * 2;
+  static constexpr int SUBS = D == 128 ? 6 : 10;  // K in the even slots, V in the odd ones
   static constexpr int SMEM_BYTES = ROFF + SUBS * kTile * D;
   static constexpr int OCOL = 2 * kTile;                    // TMEM: two S, then O
   static constexpr int COLS = 512;
 };
 
+__device__ __forceinline__ __half2 as_half2(uint32_t x) { return *reinterpret_cast<const __half2*>(&x); }
+
 template <int D>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(kPromptThreads, 1)
     kv_prompt_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                      const Params p) {
   using G = Geo<D>;
   constexpr int SUBS = G::SUBS;
   extern __shared__ __align__(1024) uint8_t smem[];
-  __shared__ __align__(8) uint64_t full[SUBS], empty[SUBS], s_full[2], s_empty[2], q_full, p_full, pv_done, drained;
+  __shared__ __align__(8) uint64_t full[SUBS], empty[SUBS], s_full[2], s_empty[2], v_full[2], v_empty[2], q_full, p_full, pv_done,
+      drained;
   __shared__ Heads heads;
-  __shared__ RangeScratch scratch;
+  __shared__ RangeScratch<kPromptThreads> scratch;
   __shared__ uint32_t tmem_s;
   __shared__ volatile int abort_flag;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -56,6 +68,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int i = 0; i < 2; ++i) {
       mbar_init(&s_full[i], 1);
       mbar_init(&s_empty[i], 4);
+      mbar_init(&v_full[i], 1);
+      mbar_init(&v_empty[i], 1);
     }
     mbar_init(&q_full, 4);
     mbar_init(&p_full, 4);
@@ -77,7 +91,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   pdl_trigger();  // after this CTA's TMEM allocation
   const uint32_t tmem = tmem_s;
   Pieces<kRows> it;
-  range_of_cta<kRows>(p, group, it, scratch);
+  range_of_cta<kPromptThreads, kRows>(p, group, it, scratch);
 
   bool ok = true;
   int gc = 0;  // tiles of the CTA so far, the same count in every role
@@ -90,9 +104,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     copy_tiles<D, SUBS, kRows>(p, group, it, &tm_k, &tm_v, smem + G::ROFF, full, empty, heads, &abort_flag);
   } else if (warp == 5) {
     // ------------------------------------------------------------ products
-    // A = P is E5M2 (bit 7), B = V is MN-major (bit 16)
     constexpr uint32_t idesc_s = idesc_e4m3(kRows, kTile, false);
-    constexpr uint32_t idesc_o = idesc_e4m3(kRows, D, false) | (1u << 7) | (1u << 16);
+    // kind::f16 with F16 operands and fp32 accumulation, V MN-major (bit 16)
+    constexpr uint32_t idesc_o = (1u << 4) | (1u << 16) | ((uint32_t)(D >> 3) << 17) | ((kRows >> 4) << 24);
     constexpr uint32_t layout = D == 128 ? 2 : 4;  // swizzle of rows of D bytes
     const uint32_t base = smem_u32(smem), ring = base + G::ROFF;
     int sub = 0;
@@ -124,41 +138,79 @@ __global__ void __launch_bounds__(kThreads, 1)
       q_phase ^= 1;
       product_s(gc);
       for (int i = 0; i < nt && ok; ++i, ++gc) {
-        advance();  // to V of this tile
-        const int v_sub = sub;
-        const uint32_t v_phase = phase;
         advance();
+        advance();  // (V's slot is the widening warps')
         if (i + 1 < nt) product_s(gc + 1);
-        if (!wait(&full[v_sub], v_phase) || !wait(&heads.full[gc & (kHeads - 1)], gc / kHeads & 1)) break;
-        // rows past the sequence hold anything, and 0 * NaN would spread: zeros instead
-        const int key0 = (it.t0 + i) * kTile;
-        if (key0 + kTile > it.limit || heads.vrange[gc & (kHeads - 1)].x == kNoPage) {
-          for (int r = lane; r < kTile; r += 32)
-            if (key0 + r >= it.limit || heads.vexp[gc & (kHeads - 1)][r >> p.shift] == kNoPage) {
-#pragma unroll
-              for (int c = 0; c < D / 16; ++c)
-                *reinterpret_cast<uint4*>(smem + G::ROFF + v_sub * kTile * D + r * D + c * 16) =
-                    make_uint4(0, 0, 0, 0);
-            }
-          fence_proxy_async_smem();
-          __syncwarp();
-        }
-        if (!wait(&p_full, gc & 1)) break;
+        if (!wait(&v_full[gc & 1], (gc >> 1) & 1) || !wait(&p_full, gc & 1)) break;
         tc_fence_after();
 #pragma unroll
-        for (int t = 0; t < 3; ++t)
-#pragma unroll
-          for (int k = 0; k < kTile / 32; ++k)
-            ew_mma_e4m3(tmem + G::OCOL, smem_desc(base + G::POFF + t * kRows * kTile + k * 32, 16, 1024, 2),
-                        smem_desc(ring + v_sub * kTile * D + k * 32 * D, 0, 8 * D, layout),
-                        idesc_o, i > 0 || t > 0 || k > 0);
-        ew_commit(&empty[v_sub]);
+        for (int k = 0; k < kTile / 16; ++k)
+          ew_mma_bf16_ss(tmem + G::OCOL,
+                         smem_desc(base + G::POFF + (k >> 2) * (kRows * 128) + (k & 3) * 32, 16, 1024, 2),
+                         smem_desc(base + G::VOFF + (gc & 1) * (kTile * D * 2) + k * 2048, kTile * 128, 1024, 2), idesc_o,
+                         i > 0 || k > 0);
+        ew_commit(&v_empty[gc & 1]);
         ew_commit(&pv_done);
       }
     }
     if (!ok && issued) {  // given up: no product may outlive the operands and the TMEM
       ew_commit(&drained);
       mbar_wait(&drained, 0);
+    }
+  } else if (warp > 5) {
+    // ------------------------------------------------------------ V to f16
+    const int th = tid - 6 * 32;
+    int sub = 1, unit = -127;
+    uint32_t phase = 0;
+    while (it.next(p, group)) {
+      unit = -127;
+      for (int i = 0; i < it.nt; ++i, ++gc) {
+        const int key0 = (it.t0 + i) * kTile, hd = gc & (kHeads - 1);
+        wait(&full[sub], phase);
+        wait(&heads.full[hd], gc / kHeads & 1);
+        wait(&v_empty[gc & 1], ((gc >> 1) & 1) ^ 1);
+        const int2 vr = heads.vrange[hd];
+        unit = max(unit, vr.y);
+        const bool plain = vr.x == unit && key0 + kTile <= it.limit;
+        const uint8_t* src = smem + G::ROFF + sub * kTile * D;
+        uint8_t* dst = smem + G::VOFF + (gc & 1) * (kTile * D * 2);
+#pragma unroll
+        for (int n = 0; n < D / 16; ++n) {
+          constexpr int CPR = D / 16;  // chunks of 16 elements of a row
+          const int r = (n * 128 + th) / CPR, c = (n * 128 + th) % CPR;
+          const uint4 w = *reinterpret_cast<const uint4*>(src + swizzled<D>(r, c));
+          uint32_t h[8];
+          decode4(w.x, h[0], h[1]);
+          decode4(w.y, h[2], h[3]);
+          decode4(w.z, h[4], h[5]);
+          decode4(w.w, h[6], h[7]);
+          if (!plain) {
+            // rows past the sequence hold anything, and 0 * NaN would spread: zeros instead
+            const int ve = heads.vexp[hd][r >> p.shift];
+            const bool there = key0 + r < it.limit && ve != kNoPage;
+            const __half2 f = __float2half2_rn(there ? exp2_int(max(ve - unit, kFarExp)) : 0.0f);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+              const __half2 y = __hmul2(as_half2(h[k]), f);
+              h[k] = there ? *reinterpret_cast<const uint32_t*>(&y) : 0u;
+            }
+          }
+          uint8_t* row = dst + (c >> 2) * (kTile * 128);
+          *reinterpret_cast<uint4*>(row + swizzled<128>(r, (c & 3) * 2)) = make_uint4(h[0], h[1], h[2], h[3]);
+          *reinterpret_cast<uint4*>(row + swizzled<128>(r, (c & 3) * 2 + 1)) = make_uint4(h[4], h[5], h[6], h[7]);
+        }
+        fence_proxy_async_smem();
+        asm volatile("bar.sync 2, 128;" ::: "memory");
+        if (warp == 6) {
+          ew_arrive(&empty[sub]);
+          ew_arrive(&v_full[gc & 1]);
+        }
+        sub += 2;
+        if (sub >= SUBS) {
+          sub -= SUBS;
+          phase ^= 1;
+        }
+      }
     }
   } else {
     // ------------------------------------------------------------ softmax, a row per thread
@@ -224,38 +276,49 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int key0 = (it.t0 + i) * kTile, buf = gc & 1, hd = gc & (kHeads - 1);
         wait(&s_full[buf], (gc >> 1) & 1);
         tc_fence_after();
-        float s[kTile];
-#pragma unroll
-        for (int c = 0; c < kTile; c += 32) {
-          uint32_t x[32];
-          tmem_ld_32x32b_x32(lane_tmem + buf * kTile + c, x);
-          tmem_ld_wait();
-#pragma unroll
-          for (int j = 0; j < 32; ++j) s[c + j] = __uint_as_float(x[j]);
-        }
-        tc_fence_before();
-        __syncwarp();
-        ew_arrive(&s_empty[buf]);
         wait(&heads.full[hd], gc / kHeads & 1);
         const int2 vr = heads.vrange[hd];
-        if (key0 + kTile > all_see || vr.x == kNoPage) {
-          const int seen = lim - key0;
+        // the row's logits, 32 keys at a time, twice: for the maximum, then for the
+        // weights (128 of them at once would not leave room for the other warps)
+        const uint32_t s_tmem = lane_tmem + buf * kTile;
+        const int seen = lim - key0;
+        const bool diagonal = key0 + kTile > all_see, holes = vr.x == kNoPage;
+        auto hide = [&](uint32_t (&x)[32], int k) {  // keys that the row does not see are -inf
+          if (diagonal) {
 #pragma unroll
-          for (int j = 0; j < kTile; ++j)
-            if (j >= seen || heads.vexp[hd][j >> p.shift] == kNoPage) s[j] = -INFINITY;
-        }
-        // log2 units: s * qs * the page's scale, 16 keys at a time
-        float c[8], top = -INFINITY;
+            for (int j = 0; j < 32; ++j)
+              if (32 * k + j >= seen) x[j] = 0xFF800000u;
+          }
+          if (holes) {
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
+            for (int h = 0; h < 2; ++h) {
+              const bool gone = heads.vexp[hd][(32 * k + 16 * h) >> p.shift] == kNoPage;
+#pragma unroll
+              for (int j = 0; j < 16; ++j) x[16 * h + j] = gone ? 0xFF800000u : x[16 * h + j];
+            }
+          }
+        };
+        float c[8], top = -INFINITY;  // log2 units per unit of S, 16 keys at a time
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
           c[k] = fminf(fmaxf(qs * heads.kscale[hd][k * 16 >> p.shift], 1.175494351e-38f), 3.402823466e38f);
-          float mx = s[16 * k];
+        uint32_t x[2][32];
+        tmem_ld_32x32b_x32(s_tmem, x[0]);
 #pragma unroll
-          for (int j = 1; j < 16; ++j) mx = fmaxf(mx, s[16 * k + j]);
-          top = fmaxf(top, mx * c[k]);
+        for (int k = 0; k < 4; ++k) {
+          tmem_ld_wait();
+          tmem_ld_32x32b_x32(s_tmem + (k < 3 ? 32 * (k + 1) : 0), x[(k + 1) & 1]);  // the next, at last the first again
+          hide(x[k & 1], k);
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            float mx = __uint_as_float(x[k & 1][16 * h]);
+#pragma unroll
+            for (int j = 1; j < 16; ++j) mx = fmaxf(mx, __uint_as_float(x[k & 1][16 * h + j]));
+            top = fmaxf(top, mx * c[2 * k + h]);
+          }
         }
         const int unit1 = max(unit, vr.y);
-        if (__any_sync(0xFFFFFFFFu, top > ref + kSlack || (m == -INFINITY && top != -INFINITY)) || unit1 != unit) {
+        if (__any_sync(0xFFFFFFFFu, top > ref + kRowSlack || (m == -INFINITY && top != -INFINITY)) || unit1 != unit) {
           // the references move to the maxima, sums and outputs with them
           const float m1 = fmaxf(m, top), r1 = m1 == -INFINITY ? 0.0f : m1, f = ex2(m - r1);
           l *= f;
@@ -265,55 +328,52 @@ __global__ void __launch_bounds__(kThreads, 1)
             const float fo = f * exp2_int(max(unit - unit1, -127));
             wait(&pv_done, (gc & 1) ^ 1);
             tc_fence_after();
+            tmem_ld_wait();
 #pragma unroll 1
             for (int o = 0; o < D; o += 32) {
-              uint32_t x[32];
-              tmem_ld_32x32b_x32(lane_tmem + G::OCOL + o, x);
+              uint32_t y[32];
+              tmem_ld_32x32b_x32(lane_tmem + G::OCOL + o, y);
               tmem_ld_wait();
 #pragma unroll
-              for (int j = 0; j < 32; ++j) x[j] = __float_as_uint(__uint_as_float(x[j]) * fo);
-              tmem_st_32x32b_x32(lane_tmem + G::OCOL + o, x);
+              for (int j = 0; j < 32; ++j) y[j] = __float_as_uint(__uint_as_float(y[j]) * fo);
+              tmem_st_32x32b_x32(lane_tmem + G::OCOL + o, y);
             }
             tmem_st_wait();
             tc_fence_before();
           }
           unit = unit1;
         }
-        const float up = kBoost - ref;
+        const float up = kRowBoost - ref;
         float sum[4] = {};
-#pragma unroll
-        for (int j = 0; j < kTile; ++j) {
-          s[j] = ex2(fmaf(s[j], c[j / 16], up));
-          sum[j & 3] += s[j];
-        }
-        l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-        if (vr.x != unit) {  // (some block of the tile is below the largest)
-#pragma unroll
-          for (int k = 0; k < 8; ++k) {
-            const float vf = exp2_int(max(heads.vexp[hd][k * 16 >> p.shift] - unit, kFarExp));
-#pragma unroll
-            for (int j = 0; j < 16; ++j) s[16 * k + j] *= vf;
-          }
-        }
         wait(&pv_done, (gc & 1) ^ 1);  // the last product has read P
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          uint32_t w1[4], w2[4], w3[4];
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const float* x = s + 16 * k + 4 * j;
-            __half2 a = __floats2half2_rn(x[0], x[1]), b = __floats2half2_rn(x[2], x[3]);
-            w1[j] = encode_e5m2(a, b);
-            a = __hsub2(a, e5m2_pair(w1[j], 0));
-            b = __hsub2(b, e5m2_pair(w1[j], 1));
-            w2[j] = encode_e5m2(a, b);
-            w3[j] = encode_e5m2(__hsub2(a, e5m2_pair(w2[j], 0)), __hsub2(b, e5m2_pair(w2[j], 1)));
+        for (int k = 0; k < 4; ++k) {
+          tmem_ld_wait();
+          if (k < 3) {
+            tmem_ld_32x32b_x32(s_tmem + 32 * (k + 1), x[(k + 1) & 1]);
+          } else {
+            tc_fence_before();
+            __syncwarp();
+            ew_arrive(&s_empty[buf]);
           }
-          uint8_t* dst = smem + G::POFF + swizzled<128>(tid, k);
-          *reinterpret_cast<uint4*>(dst) = make_uint4(w1[0], w1[1], w1[2], w1[3]);
-          *reinterpret_cast<uint4*>(dst + kRows * kTile) = make_uint4(w2[0], w2[1], w2[2], w2[3]);
-          *reinterpret_cast<uint4*>(dst + 2 * kRows * kTile) = make_uint4(w3[0], w3[1], w3[2], w3[3]);
+          hide(x[k & 1], k);
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            uint32_t w[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const int n = 8 * q + 2 * j;
+              const float a = ex2(fmaf(__uint_as_float(x[k & 1][n]), c[2 * k + q / 2], up));
+              const float b = ex2(fmaf(__uint_as_float(x[k & 1][n + 1]), c[2 * k + q / 2], up));
+              sum[j] += a + b;
+              const __half2 h = __floats2half2_rn(a, b);
+              w[j] = *reinterpret_cast<const uint32_t*>(&h);
+            }
+            *reinterpret_cast<uint4*>(smem + G::POFF + (k >> 1) * (kRows * 128) +
+                                      swizzled<128>(tid, (k & 1) * 4 + q)) = make_uint4(w[0], w[1], w[2], w[3]);
+          }
         }
+        l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
         fence_proxy_async_smem();
         __syncwarp();
         ew_arrive(&p_full);
@@ -323,7 +383,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool whole = it.take == it.span, none = l == 0.0f;
       const int64_t part = ((int64_t)blockIdx.x * 2 + (first ? 0 : 1)) * kRows + tid;
       const float inv = none ? 0.0f : reciprocal(l), us = exp2_int(unit);
-      const float lse2 = none ? -INFINITY : ref + (lg2(l) - kBoost);
+      const float lse2 = none ? -INFINITY : ref + (lg2(l) - kRowBoost);
       if (live) {
         if (!whole) p.part_lse[part] = lse2;
         else if (p.lse != nullptr) p.lse[at] = lse2 * 0.6931471805599453f;
@@ -374,7 +434,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 template <int D>
 cudaError_t launch_prompt(const KvAttention& a, cudaStream_t st) {
-  return launch<D, kRows>(kv_prompt_kernel<D>, 1, Geo<D>::SMEM_BYTES, a, st);
+  return launch<D, kRows>(kv_prompt_kernel<D>, 1, kPromptThreads, Geo<D>::SMEM_BYTES, a, st);
 }
 
 }  // namespace
