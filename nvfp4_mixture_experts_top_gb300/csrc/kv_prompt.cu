@@ -174,7 +174,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
         const bool plain = vr.x == unit && key0 + kTile <= it.limit;
         const uint8_t* src = smem + G::ROFF + sub * kTile * D;
         uint8_t* dst = smem + G::VOFF + (gc & 1) * (kTile * D * 2);
-#pragma unroll
+#pragma unroll 2
         for (int n = 0; n < D / 16; ++n) {
           constexpr int CPR = D / 16;  // chunks of 16 elements of a row
           const int r = (n * 128 + th) / CPR, c = (n * 128 + th) % CPR;
@@ -230,15 +230,16 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
       if (nt > 0) {
         const uint4* src = reinterpret_cast<const uint4*>(p.q + (int64_t)(it.rq.q0 + tok) * p.ld_q +
                                                           (int64_t)(it.hk * group + rr - tok * group) * D);
-        uint4 w[D / 8];
         float amax = 0.0f;
+        if (live) {
+#pragma unroll 4
+          for (int i = 0; i < D / 8; ++i) {
+            const uint4 w = src[i];
+            const uint32_t x[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
-        for (int i = 0; i < D / 8; ++i) {
-          w[i] = live ? src[i] : make_uint4(0, 0, 0, 0);
-          const uint32_t x[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
-#pragma unroll
-          for (int k = 0; k < 4; ++k)
-            amax = fmaxf(amax, fmaxf(fabsf(__uint_as_float(x[k] << 16)), fabsf(__uint_as_float(x[k] & 0xFFFF0000u))));
+            for (int k = 0; k < 4; ++k)
+              amax = fmaxf(amax, fmaxf(fabsf(__uint_as_float(x[k] << 16)), fabsf(__uint_as_float(x[k] & 0xFFFF0000u))));
+          }
         }
         const int e = amax == 0.0f ? 0 : min(7 - floor_log2(amax), 126);
         float f = exp2_int(e);
@@ -246,20 +247,22 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
         if (!(amax <= 3.402823466e38f)) f = __int_as_float(0x7FFFFFFF);
         // (a zero scale stays apart from a key that is not seen: -inf * qs)
         qs = fmaxf(fabsf(p.scale) * 1.4426950408889634f * exp2_int(-e), 1.175494351e-38f);
-#pragma unroll
+#pragma unroll 1
         for (int c = 0; c < D / 16; ++c) {
-          uint32_t hi[4], lo[4];
+          uint32_t hi[4] = {}, lo[4] = {};
+          if (live) {
+            const uint4 v[2] = {src[2 * c], src[2 * c + 1]};
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const uint4 v = w[2 * c + (i >> 1)];
-            const uint32_t a = i & 1 ? v.z : v.x, b = i & 1 ? v.w : v.y;
-            const float x0 = __uint_as_float(a << 16) * f, x1 = __uint_as_float(a & 0xFFFF0000u) * f;
-            const float x2 = __uint_as_float(b << 16) * f, x3 = __uint_as_float(b & 0xFFFF0000u) * f;
-            hi[i] = encode4(x0, x1, x2, x3);
-            uint32_t d0, d1;
-            decode4(hi[i], d0, d1);
-            const float2 y0 = f16x2_to_f32(d0), y1 = f16x2_to_f32(d1);
-            lo[i] = encode4(x0 - y0.x, x1 - y0.y, x2 - y1.x, x3 - y1.y);
+            for (int i = 0; i < 4; ++i) {
+              const uint32_t a = i & 1 ? v[i >> 1].z : v[i >> 1].x, b = i & 1 ? v[i >> 1].w : v[i >> 1].y;
+              const float x0 = __uint_as_float(a << 16) * f, x1 = __uint_as_float(a & 0xFFFF0000u) * f;
+              const float x2 = __uint_as_float(b << 16) * f, x3 = __uint_as_float(b & 0xFFFF0000u) * f;
+              hi[i] = encode4(x0, x1, x2, x3);
+              uint32_t d0, d1;
+              decode4(hi[i], d0, d1);
+              const float2 y0 = f16x2_to_f32(d0), y1 = f16x2_to_f32(d1);
+              lo[i] = encode4(x0 - y0.x, x1 - y0.y, x2 - y1.x, x3 - y1.y);
+            }
           }
           *reinterpret_cast<uint4*>(smem + G::QOFF + swizzled<D>(tid, c)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
           *reinterpret_cast<uint4*>(smem + G::QOFF + kRows * D + swizzled<D>(tid, c)) =
@@ -279,43 +282,37 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
         wait(&heads.full[hd], gc / kHeads & 1);
         const int2 vr = heads.vrange[hd];
         // the row's logits, 32 keys at a time, twice: for the maximum, then for the
-        // weights (128 of them at once would not leave room for the other warps)
+        // weights.  Loops stay rolled: unrolled, the roles' code outgrew the
+        // instruction cache, and half of all issue slots were lost to it.
         const uint32_t s_tmem = lane_tmem + buf * kTile;
         const int seen = lim - key0;
-        const bool diagonal = key0 + kTile > all_see, holes = vr.x == kNoPage;
+        const bool odd = key0 + kTile > all_see || vr.x == kNoPage;
         auto hide = [&](uint32_t (&x)[32], int k) {  // keys that the row does not see are -inf
-          if (diagonal) {
+          const bool gone0 = heads.vexp[hd][k >> p.shift] == kNoPage;
+          const bool gone1 = heads.vexp[hd][(k + 16) >> p.shift] == kNoPage;
 #pragma unroll
-            for (int j = 0; j < 32; ++j)
-              if (32 * k + j >= seen) x[j] = 0xFF800000u;
-          }
-          if (holes) {
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              const bool gone = heads.vexp[hd][(32 * k + 16 * h) >> p.shift] == kNoPage;
-#pragma unroll
-              for (int j = 0; j < 16; ++j) x[16 * h + j] = gone ? 0xFF800000u : x[16 * h + j];
-            }
-          }
+          for (int j = 0; j < 32; ++j)
+            if (k + j >= seen || (j < 16 ? gone0 : gone1)) x[j] = 0xFF800000u;
         };
-        float c[8], top = -INFINITY;  // log2 units per unit of S, 16 keys at a time
-#pragma unroll
-        for (int k = 0; k < 8; ++k)
-          c[k] = fminf(fmaxf(qs * heads.kscale[hd][k * 16 >> p.shift], 1.175494351e-38f), 3.402823466e38f);
-        uint32_t x[2][32];
-        tmem_ld_32x32b_x32(s_tmem, x[0]);
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
+        // log2 units per unit of S
+        auto factor = [&](int k) {
+          return fminf(fmaxf(qs * heads.kscale[hd][k >> p.shift], 1.175494351e-38f), 3.402823466e38f);
+        };
+        float top = -INFINITY;
+#pragma unroll 1
+        for (int k = 0; k < kTile; k += 32) {
+          uint32_t x[32];
+          tmem_ld_32x32b_x32(s_tmem + k, x);
+          const float c0 = factor(k), c1 = factor(k + 16);
           tmem_ld_wait();
-          tmem_ld_32x32b_x32(s_tmem + (k < 3 ? 32 * (k + 1) : 0), x[(k + 1) & 1]);  // the next, at last the first again
-          hide(x[k & 1], k);
+          if (odd) hide(x, k);
+          float mx[8];
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            float mx = __uint_as_float(x[k & 1][16 * h]);
-#pragma unroll
-            for (int j = 1; j < 16; ++j) mx = fmaxf(mx, __uint_as_float(x[k & 1][16 * h + j]));
-            top = fmaxf(top, mx * c[2 * k + h]);
-          }
+          for (int j = 0; j < 8; ++j)
+            mx[j] = fmaxf(fmaxf(__uint_as_float(x[4 * j]), __uint_as_float(x[4 * j + 1])),
+                          fmaxf(__uint_as_float(x[4 * j + 2]), __uint_as_float(x[4 * j + 3])));
+          top = fmaxf(top, fmaxf(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * c0,
+                                 fmaxf(fmaxf(mx[4], mx[5]), fmaxf(mx[6], mx[7])) * c1));
         }
         const int unit1 = max(unit, vr.y);
         if (__any_sync(0xFFFFFFFFu, top > ref + kRowSlack || (m == -INFINITY && top != -INFINITY)) || unit1 != unit) {
@@ -328,7 +325,6 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
             const float fo = f * exp2_int(max(unit - unit1, -127));
             wait(&pv_done, (gc & 1) ^ 1);
             tc_fence_after();
-            tmem_ld_wait();
 #pragma unroll 1
             for (int o = 0; o < D; o += 32) {
               uint32_t y[32];
@@ -346,33 +342,32 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
         const float up = kRowBoost - ref;
         float sum[4] = {};
         wait(&pv_done, (gc & 1) ^ 1);  // the last product has read P
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
+#pragma unroll 1
+        for (int k = 0; k < kTile; k += 32) {
+          uint32_t x[32];
+          tmem_ld_32x32b_x32(s_tmem + k, x);
+          const float c0 = factor(k), c1 = factor(k + 16);
           tmem_ld_wait();
-          if (k < 3) {
-            tmem_ld_32x32b_x32(s_tmem + 32 * (k + 1), x[(k + 1) & 1]);
-          } else {
-            tc_fence_before();
-            __syncwarp();
-            ew_arrive(&s_empty[buf]);
-          }
-          hide(x[k & 1], k);
+          if (odd) hide(x, k);
+          uint8_t* dst = smem + G::POFF + (k >> 6) * (kRows * 128);
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
             uint32_t w[4];
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
               const int n = 8 * q + 2 * j;
-              const float a = ex2(fmaf(__uint_as_float(x[k & 1][n]), c[2 * k + q / 2], up));
-              const float b = ex2(fmaf(__uint_as_float(x[k & 1][n + 1]), c[2 * k + q / 2], up));
+              const float a = ex2(fmaf(__uint_as_float(x[n]), q < 2 ? c0 : c1, up));
+              const float b = ex2(fmaf(__uint_as_float(x[n + 1]), q < 2 ? c0 : c1, up));
               sum[j] += a + b;
               const __half2 h = __floats2half2_rn(a, b);
               w[j] = *reinterpret_cast<const uint32_t*>(&h);
             }
-            *reinterpret_cast<uint4*>(smem + G::POFF + (k >> 1) * (kRows * 128) +
-                                      swizzled<128>(tid, (k & 1) * 4 + q)) = make_uint4(w[0], w[1], w[2], w[3]);
+            *reinterpret_cast<uint4*>(dst + swizzled<128>(tid, (k >> 3 & 4) + q)) = make_uint4(w[0], w[1], w[2], w[3]);
           }
         }
+        tc_fence_before();
+        __syncwarp();
+        ew_arrive(&s_empty[buf]);
         l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
         fence_proxy_async_smem();
         __syncwarp();
