@@ -104,9 +104,44 @@ struct Shares {
   }
 };
 
-// Walks the pieces of sequences that a range of the work consists of.  A sequence
-// counts kPieceCost and its tiles; a cut inside the cost falls before its first
-// tile.
+// A request's work.  A sequence (a tile of R rows of a K/V head) counts kPieceCost and
+// its tiles of keys.  A tile of 128 rows has 128 / group more keys than the one before
+// it, so work is counted in 1 / group of a tile there, and sequence t of a head
+// counts t more than its first one.  (Counting every sequence as long as the last
+// one, the CTAs of three chunks of 1.5-2.1K tokens were busy for 78% of the time.)
+template <int R>
+struct Work {
+  static constexpr bool kGrows = R == 128;
+  int unit, base, tiles;  // of a tile; of a head's first sequence; sequences of a head
+  int64_t head;           // of a head
+  __device__ __forceinline__ Work(const Request& r, int group) {
+    const int rows = r.n * group;
+    unit = kGrows ? group : 1;
+    tiles = (rows + R - 1) / R;
+    const int keys = kGrows ? min(r.kv, r.kv - r.n + (min(R, rows) - 1) / group + 1) : r.kv;
+    base = (kPieceCost + (keys > kTile ? (keys - 1) / kTile + 1 : 1)) * unit;
+    head = start(tiles);
+  }
+  __device__ __forceinline__ int64_t start(int t) const {  // of a head's first t sequences
+    return (int64_t)t * base + (kGrows ? (int64_t)t * (t - 1) / 2 : 0);
+  }
+  __device__ __forceinline__ int64_t start_of(int64_t seq) const {
+    const int64_t h = divide(seq, tiles);
+    return h * head + start((int)(seq - h * tiles));
+  }
+  __device__ __forceinline__ int find(int64_t at) const {  // the sequence of a head that holds `at`
+    if (tiles == 1) return 0;
+    if (!kGrows) return (int)divide(at, base);
+    const float b = base - 0.5f, x = (float)at;
+    int t = min((int)(2.0f * x / (b + sqrtf(b * b + 2.0f * x))), tiles - 1);
+    while (start(t) > at) --t;
+    while (start(t + 1) <= at) ++t;
+    return t;
+  }
+};
+
+// Walks the pieces of sequences that a range of the work consists of.  A cut inside a
+// tile falls on the tile's start, one inside the cost before its first tile.
 template <int R>
 struct Pieces {
   int b;         // request
@@ -116,36 +151,34 @@ struct Pieces {
   Request rq;
   int hk, row0, nrows, span, u0, take;
   int limit;     // keys that the last row of the tile sees
-  int t0, nt;    // its tiles (fewer than it counts where the rows see fewer keys)
+  int t0, nt;    // its tiles
 
-  __device__ __forceinline__ static int span_of(int kv) {
-    return kPieceCost + (kv > kTile ? (kv - 1) / kTile + 1 : 1);
-  }
-  __device__ __forceinline__ static int row_tiles(int n, int group) { return (n * group + R - 1) / R; }
   __device__ __forceinline__ bool next(const Params& p, int group) {
     if (left <= 0) return false;
-    int tiles;
     for (;; ++b) {
       if (b >= p.B) return false;
       rq = get_request(p, b);
-      span = span_of(rq.kv);
-      tiles = row_tiles(rq.n, group);
-      const int64_t w = (int64_t)tiles * p.Hkv * span;
-      if (off < w) break;
-      off -= w;
+      const Work<R> w(rq, group);
+      if (off >= w.head * p.Hkv) {
+        off -= w.head * p.Hkv;
+        continue;
+      }
+      hk = (int)divide(off, w.head);
+      const int64_t in = off - hk * w.head;
+      const int t = w.find(in);
+      span = w.base + (w.kGrows ? t : 0);
+      u0 = (int)(in - w.start(t));
+      take = (int)min((int64_t)(span - u0), left);
+      row0 = t * R;
+      nrows = min(R, rq.n * group - row0);
+      limit = rq.n == 1 ? rq.kv : min(rq.kv, rq.kv - rq.n + (row0 + nrows - 1) / group + 1);
+      const int tiles = limit > 0 ? (limit - 1) / kTile + 1 : 0;
+      t0 = min(max(u0 / w.unit - kPieceCost, 0), tiles);
+      nt = (u0 + take == span ? tiles : min(max((u0 + take) / w.unit - kPieceCost, 0), tiles)) - t0;
+      off += take;
+      left -= take;
+      return true;
     }
-    const int seq = (int)divide(off, span);
-    u0 = (int)(off - (int64_t)seq * span);
-    take = (int)min((int64_t)(span - u0), left);
-    hk = tiles == 1 ? seq : seq / tiles;
-    row0 = (seq - hk * tiles) * R;
-    nrows = min(R, rq.n * group - row0);
-    limit = rq.n == 1 ? rq.kv : min(rq.kv, rq.kv - rq.n + (row0 + nrows - 1) / group + 1);
-    t0 = max(u0 - kPieceCost, 0);
-    nt = max(min(u0 + take - kPieceCost, limit > 0 ? (limit - 1) / kTile + 1 : 0) - t0, 0);
-    off += take;
-    left -= take;
-    return true;
   }
 };
 
@@ -169,10 +202,10 @@ __device__ __forceinline__ void range_of_cta(const Params& p, int group, Pieces<
   bool bad = false;
   for (int b = b0; b < b1; ++b) {
     const Request r = get_request(p, b);
-    const int n = Pieces<R>::row_tiles(r.n, group) * p.Hkv;
-    seqs += n;
-    work += (int64_t)n * Pieces<R>::span_of(r.kv);
-    if (n) longest = max(longest, r.kv);
+    const Work<R> w(r, group);
+    seqs += (int64_t)w.tiles * p.Hkv;
+    work += w.head * p.Hkv;
+    if (w.tiles) longest = max(longest, r.kv);
     bad |= r.bad;
   }
   if (bad && blockIdx.x == 0) report_status(p.dev_status, NVFP4_E_BAD_PAGE);
@@ -202,15 +235,14 @@ __device__ __forceinline__ void range_of_cta(const Params& p, int group, Pieces<
     const int64_t lo = sh.start(c), n = sh.start(c + 1) - lo;
     if (before <= lo && lo < before + (split ? work : seqs)) {
       for (int b = b0; b < b1; ++b) {
-        const Request r = get_request(p, b);
-        const int span = Pieces<R>::span_of(r.kv);
-        const int64_t seqs_b = (int64_t)Pieces<R>::row_tiles(r.n, group) * p.Hkv, w = split ? seqs_b * span : seqs_b;
-        if (lo < before + w) {
+        const Work<R> w(get_request(p, b), group);
+        const int64_t n = (split ? w.head : w.tiles) * p.Hkv;
+        if (lo < before + n) {
           x.b = b;
-          x.off = split ? lo - before : (lo - before) * span;
+          x.off = lo - before;
           break;
         }
-        before += w;
+        before += n;
       }
     }
     __syncthreads();
@@ -218,15 +250,16 @@ __device__ __forceinline__ void range_of_cta(const Params& p, int group, Pieces<
     it.off = x.off;
     it.left = n;
     if (!split) {  // sequences to work
-      int64_t rest = n, skip = -1;
+      int64_t rest = n, skip = it.off;
       it.left = 0;
       for (int b = it.b; b < p.B && rest > 0; ++b) {
-        const Request r = get_request(p, b);
-        const int span = Pieces<R>::span_of(r.kv);
-        if (skip < 0) skip = divide(it.off, span);
-        const int64_t k = min(rest, (int64_t)Pieces<R>::row_tiles(r.n, group) * p.Hkv - skip);
+        const Work<R> w(get_request(p, b), group);
+        const int64_t k = min(rest, (int64_t)w.tiles * p.Hkv - skip);
+        if (k <= 0) continue;
+        const int64_t from = w.start_of(skip);
+        if (b == it.b) it.off = from;
+        it.left += w.start_of(skip + k) - from;
         skip = 0;
-        it.left += k * span;
         rest -= k;
       }
     }

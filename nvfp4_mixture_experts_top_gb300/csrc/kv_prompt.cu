@@ -2,7 +2,8 @@
 // per request and K/V head (prompt chunks): a tile of 128 rows against tiles of 128
 // keys, S = Q K^T and O += P V on tcgen05 with the cached codes as they are.
 //
-// A row is a lane: its maximum, sum and reference are a thread's own.
+// A row is a lane; two threads share it, one for each half of a tile's keys, and
+// agree on its reference.
 //   S = Q K^T   K's codes as they are (kind::f8f6f4), the query row as the sum of two
 //               E4M3 values times its power of two, 2^-e (q1 + q2): exact for what
 //               bf16 holds down to 2^-9 of the row's largest element, within 2^-17
@@ -15,8 +16,8 @@
 // quarter per cycle and scheduler); S and V's f16 form are double buffered so that
 // all run at a time.
 //
-// Roles, ring, division of the work and join as in kv_attention.cu, and warps 6-9 that
-// widen V; one CTA per SM.
+// Ring, division of the work and join as in kv_attention.cu; one CTA per SM.  Warps
+// 0-7 softmax, 8 copies, 9 products, 12-15 widen V.
 #include "kv_attention.cuh"
 
 namespace nvfp4moe {
@@ -26,23 +27,20 @@ using namespace kv;
 
 constexpr int kRows = 128;
 
-constexpr int kPromptThreads = 320;
-constexpr float kRowSlack = 5.0f;   // log2 by which a logit may pass the row's reference
-constexpr float kRowBoost = 10.5f;  // log2 of the weights' shift: 2^(10.5 + 5) is in f16's range
+constexpr int kPromptThreads = 512;
+constexpr float kRowSlack = 10.0f;  // log2 by which a logit may pass the row's reference
+constexpr float kRowBoost = 5.5f;   // log2 of the weights' shift: 2^(5.5 + 10) is in f16's range
 
 template <int D>
 struct Geo {
-  static constexpr int QOFF = 0;                            // [2 terms][128][D] E4M3
-  static constexpr int POFF = QOFF + 2 * kRows * D;         // [2 halves of the keys][128 rows][64] f16
-  static constexpr int VOFF = POFF + kRows * kTile * 2;     // [2 buffers][D / 64][128 keys][64] f16
+  static constexpr int QOFF = 0;                             // [2 buffers][2 terms][128][D] E4M3
+  static constexpr int VOFF = QOFF + 2 * 2 * kRows * D;      // [2 buffers][D / 64][128 keys][64] f16
   static constexpr int ROFF = VOFF + 2 * kTile * D * 2;
   static constexpr int SUBS = D == 128 ? 6 : 10;  // K in the even slots, V in the odd ones
   static constexpr int SMEM_BYTES = ROFF + SUBS * kTile * D;
-  static constexpr int OCOL = 2 * kTile;                    // TMEM: two S, then O
+  static constexpr int OCOL = 2 * kTile;                     // TMEM: S (then the weights) and O of each group
   static constexpr int COLS = 512;
 };
-
-__device__ __forceinline__ __half2 as_half2(uint32_t x) { return *reinterpret_cast<const __half2*>(&x); }
 
 template <int D>
 __global__ void __launch_bounds__(kPromptThreads, 1)
@@ -51,10 +49,11 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
   using G = Geo<D>;
   constexpr int SUBS = G::SUBS;
   extern __shared__ __align__(1024) uint8_t smem[];
-  __shared__ __align__(8) uint64_t full[SUBS], empty[SUBS], s_full[2], s_empty[2], v_full[2], v_empty[2], q_full, p_full, pv_done,
-      drained;
+  __shared__ __align__(8) uint64_t full[SUBS], empty[SUBS], s_full[2], p_full[2], pv_done[2], v_full[2], q_full[2],
+      q_empty[2], drained;
   __shared__ Heads heads;
   __shared__ RangeScratch<kPromptThreads> scratch;
+  __shared__ int8_t q_exp[2][kRows];
   __shared__ uint32_t tmem_s;
   __shared__ volatile int abort_flag;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -62,25 +61,24 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
   if (tid == 0) {
     for (int i = 0; i < SUBS; ++i) {
       mbar_init(&full[i], 1);
-      mbar_init(&empty[i], 1);
+      mbar_init(&empty[i], i & 1 ? 4 : 1);
     }
     for (int i = 0; i < kHeads; ++i) mbar_init(&heads.full[i], 1);
     for (int i = 0; i < 2; ++i) {
       mbar_init(&s_full[i], 1);
-      mbar_init(&s_empty[i], 4);
-      mbar_init(&v_full[i], 1);
-      mbar_init(&v_empty[i], 1);
+      mbar_init(&p_full[i], 4);
+      mbar_init(&pv_done[i], 1);
+      mbar_init(&v_full[i], 4);
+      mbar_init(&q_full[i], 2);
+      mbar_init(&q_empty[i], 8);
     }
-    mbar_init(&q_full, 4);
-    mbar_init(&p_full, 4);
-    mbar_init(&pv_done, 1);
     mbar_init(&drained, 1);
     abort_flag = 0;
     fence_mbar_init();
     prefetch_tmap(&tm_k);
     prefetch_tmap(&tm_v);
   }
-  if (warp == 5) {
+  if (warp == 9) {
     tmem_alloc(&tmem_s, G::COLS);
     tmem_relinquish();
   }
@@ -94,15 +92,15 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
   range_of_cta<kPromptThreads, kRows>(p, group, it, scratch);
 
   bool ok = true;
-  int gc = 0;  // tiles of the CTA so far, the same count in every role
+  int gc = 0, qn = 0;  // tiles and pieces of the CTA so far, the same counts in every role
   auto wait = [&](uint64_t* bar, uint32_t parity) {
     // (after a failure the softmax warps go on without waiting)
     if (ok) ok = warp_wait(bar, parity, &abort_flag, p.dev_status);
     return ok;
   };
-  if (warp == 4) {
+  if (warp == 8) {
     copy_tiles<D, SUBS, kRows>(p, group, it, &tm_k, &tm_v, smem + G::ROFF, full, empty, heads, &abort_flag);
-  } else if (warp == 5) {
+  } else if (warp == 9) {
     // ------------------------------------------------------------ products
     constexpr uint32_t idesc_s = idesc_e4m3(kRows, kTile, false);
     // kind::f16 with F16 operands and fp32 accumulation, V MN-major (bit 16)
@@ -110,181 +108,182 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
     constexpr uint32_t layout = D == 128 ? 2 : 4;  // swizzle of rows of D bytes
     const uint32_t base = smem_u32(smem), ring = base + G::ROFF;
     int sub = 0;
-    uint32_t phase = 0, q_phase = 0;
+    uint32_t phase = 0;
     bool issued = false;
-    auto advance = [&] {
-      if (++sub == SUBS) {
-        sub = 0;
-        phase ^= 1;
-      }
-    };
-    auto product_s = [&](int n) {  // S of tile n of the CTA: K's slot is the current one
-      if (!wait(&full[sub], phase) || !wait(&s_empty[n & 1], ((n >> 1) & 1) ^ 1)) return;
+    auto product_s = [&](int n) {  // S of tile n of the CTA, over the weights of tile n - 2
+      if (!wait(&full[sub], phase) || !wait(&pv_done[n & 1], ((n >> 1) & 1) ^ 1)) return;
       tc_fence_after();
+      const uint32_t q = base + G::QOFF + (qn & 1) * (2 * kRows * D);
 #pragma unroll
       for (int t = 0; t < 2; ++t)
 #pragma unroll
         for (int k = 0; k < D / 32; ++k)
-          ew_mma_e4m3(tmem + (n & 1) * kTile, smem_desc(base + G::QOFF + t * kRows * D + k * 32, 16, 8 * D, layout),
+          ew_mma_e4m3(tmem + (n & 1) * kTile, smem_desc(q + t * kRows * D + k * 32, 16, 8 * D, layout),
                       smem_desc(ring + sub * kTile * D + k * 32, 16, 8 * D, layout), idesc_s, t > 0 || k > 0);
       ew_commit(&empty[sub]);
       ew_commit(&s_full[n & 1]);
       issued = true;
+      sub += 2;  // (V's slots are the widening warps')
+      if (sub == SUBS) {
+        sub = 0;
+        phase ^= 1;
+      }
     };
     while (ok && it.next(p, group)) {
       const int nt = it.nt;
       if (nt == 0) continue;
-      if (!wait(&q_full, q_phase)) break;
-      q_phase ^= 1;
+      if (!wait(&q_full[qn & 1], (qn >> 1) & 1)) break;
       product_s(gc);
+      if (nt > 1) product_s(gc + 1);
       for (int i = 0; i < nt && ok; ++i, ++gc) {
-        advance();
-        advance();  // (V's slot is the widening warps')
-        if (i + 1 < nt) product_s(gc + 1);
-        if (!wait(&v_full[gc & 1], (gc >> 1) & 1) || !wait(&p_full, gc & 1)) break;
+        const int g = gc & 1;
+        if (!wait(&v_full[g], (gc >> 1) & 1) || !wait(&p_full[g], (gc >> 1) & 1)) break;
         tc_fence_after();
 #pragma unroll
         for (int k = 0; k < kTile / 16; ++k)
-          ew_mma_bf16_ss(tmem + G::OCOL,
-                         smem_desc(base + G::POFF + (k >> 2) * (kRows * 128) + (k & 3) * 32, 16, 1024, 2),
-                         smem_desc(base + G::VOFF + (gc & 1) * (kTile * D * 2) + k * 2048, kTile * 128, 1024, 2), idesc_o,
-                         i > 0 || k > 0);
-        ew_commit(&v_empty[gc & 1]);
-        ew_commit(&pv_done);
+          ew_mma_bf16_ts(tmem + G::OCOL + g * D, tmem + g * kTile + k * 8,
+                         smem_desc(base + G::VOFF + g * (kTile * D * 2) + k * 2048, kTile * 128, 1024, 2), idesc_o,
+                         i > 1 || k > 0);
+        ew_commit(&pv_done[g]);
+        if (i + 2 < nt) product_s(gc + 2);
       }
+      ++qn;
     }
     if (!ok && issued) {  // given up: no product may outlive the operands and the TMEM
       ew_commit(&drained);
       mbar_wait(&drained, 0);
     }
-  } else if (warp > 5) {
+  } else if (warp >= 12) {
     // ------------------------------------------------------------ V to f16
-    const int th = tid - 6 * 32;
-    int sub = 1, unit = -127;
+    // 8 lanes take 4 chunks of two rows r and r ^ 5: no bank is met twice, neither in
+    // the codes nor in their f16 form
+    const int w = warp - 12, c = (lane & 3) + (D == 128 ? (w & 1) * 4 : 0);
+    const int r0 = (D == 128 ? w >> 1 : w) * 8 + ((lane >> 3) ^ (lane & 4 ? 5 : 0));
+    int sub = 1;
     uint32_t phase = 0;
     while (it.next(p, group)) {
-      unit = -127;
       for (int i = 0; i < it.nt; ++i, ++gc) {
-        const int key0 = (it.t0 + i) * kTile, hd = gc & (kHeads - 1);
+        const int key0 = (it.t0 + i) * kTile, hd = gc & (kHeads - 1), g = gc & 1;
         wait(&full[sub], phase);
         wait(&heads.full[hd], gc / kHeads & 1);
-        wait(&v_empty[gc & 1], ((gc >> 1) & 1) ^ 1);
-        const int2 vr = heads.vrange[hd];
-        unit = max(unit, vr.y);
-        const bool plain = vr.x == unit && key0 + kTile <= it.limit;
-        const uint8_t* src = smem + G::ROFF + sub * kTile * D;
-        uint8_t* dst = smem + G::VOFF + (gc & 1) * (kTile * D * 2);
-#pragma unroll 2
-        for (int n = 0; n < D / 16; ++n) {
-          constexpr int CPR = D / 16;  // chunks of 16 elements of a row
-          const int r = (n * 128 + th) / CPR, c = (n * 128 + th) % CPR;
-          const uint4 w = *reinterpret_cast<const uint4*>(src + swizzled<D>(r, c));
+        wait(&pv_done[g], ((gc >> 1) & 1) ^ 1);
+        // rows past the sequence hold anything, and 0 * NaN would spread: zeros instead
+        const bool odd = key0 + kTile > it.limit || heads.vrange[hd].x == kNoPage;
+        const uint8_t* src = smem + G::ROFF + sub * kTile * D + swizzled<D>(r0, c);
+        uint8_t* dst = smem + G::VOFF + g * (kTile * D * 2) + (c >> 2) * (kTile * 128);
+        uint8_t* dst0 = dst + swizzled<128>(r0, (c & 3) * 2);
+        uint8_t* dst1 = dst + swizzled<128>(r0, (c & 3) * 2 + 1);
+        constexpr int STEP = D == 128 ? 16 : 32;
+#pragma unroll 4
+        for (int n = 0; n < kTile; n += STEP) {
+          uint4 x = *reinterpret_cast<const uint4*>(src + n * D);
+          if (odd && (key0 + r0 + n >= it.limit || heads.vexp[hd][(r0 + n) >> p.shift] == kNoPage))
+            x = make_uint4(0, 0, 0, 0);
           uint32_t h[8];
-          decode4(w.x, h[0], h[1]);
-          decode4(w.y, h[2], h[3]);
-          decode4(w.z, h[4], h[5]);
-          decode4(w.w, h[6], h[7]);
-          if (!plain) {
-            // rows past the sequence hold anything, and 0 * NaN would spread: zeros instead
-            const int ve = heads.vexp[hd][r >> p.shift];
-            const bool there = key0 + r < it.limit && ve != kNoPage;
-            const __half2 f = __float2half2_rn(there ? exp2_int(max(ve - unit, kFarExp)) : 0.0f);
-#pragma unroll
-            for (int k = 0; k < 8; ++k) {
-              const __half2 y = __hmul2(as_half2(h[k]), f);
-              h[k] = there ? *reinterpret_cast<const uint32_t*>(&y) : 0u;
-            }
-          }
-          uint8_t* row = dst + (c >> 2) * (kTile * 128);
-          *reinterpret_cast<uint4*>(row + swizzled<128>(r, (c & 3) * 2)) = make_uint4(h[0], h[1], h[2], h[3]);
-          *reinterpret_cast<uint4*>(row + swizzled<128>(r, (c & 3) * 2 + 1)) = make_uint4(h[4], h[5], h[6], h[7]);
+          decode4(x.x, h[0], h[1]);
+          decode4(x.y, h[2], h[3]);
+          decode4(x.z, h[4], h[5]);
+          decode4(x.w, h[6], h[7]);
+          *reinterpret_cast<uint4*>(dst0 + n * 128) = make_uint4(h[0], h[1], h[2], h[3]);
+          *reinterpret_cast<uint4*>(dst1 + n * 128) = make_uint4(h[4], h[5], h[6], h[7]);
         }
         fence_proxy_async_smem();
-        asm volatile("bar.sync 2, 128;" ::: "memory");
-        if (warp == 6) {
-          ew_arrive(&empty[sub]);
-          ew_arrive(&v_full[gc & 1]);
-        }
+        __syncwarp();
+        ew_arrive(&empty[sub]);
+        ew_arrive(&v_full[g]);
         sub += 2;
-        if (sub >= SUBS) {
-          sub -= SUBS;
+        if (sub > SUBS) {
+          sub = 1;
           phase ^= 1;
         }
       }
     }
+  } else if (warp >= 10) {
+    // ------------------------------------------------------------ query rows
+    // as 2^-e (q1 + q2), in the sign of the scale, a thread per 16 elements; a row
+    // that is not finite becomes NaN
+    constexpr int LPR = D / 16;
+    const int t = tid - 10 * 32, c = t % LPR;
+    while (it.next(p, group)) {
+      if (it.nt == 0) continue;
+      const int qb = qn & 1;
+      wait(&q_empty[qb], ((qn >> 1) & 1) ^ 1);
+      uint8_t* q8 = smem + G::QOFF + qb * (2 * kRows * D);
+#pragma unroll 2
+      for (int r = t / LPR; r < kRows; r += 64 / LPR) {
+        uint4 w[2] = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
+        if (r < it.nrows) {
+          const int qr = it.row0 + r, qt = qr / group;
+          const uint4* src = reinterpret_cast<const uint4*>(p.q + (int64_t)(it.rq.q0 + qt) * p.ld_q +
+                                                            (int64_t)(it.hk * group + qr - qt * group) * D + 16 * c);
+          w[0] = src[0];
+          w[1] = src[1];
+        }
+        const uint32_t x[8] = {w[0].x, w[0].y, w[0].z, w[0].w, w[1].x, w[1].y, w[1].z, w[1].w};
+        float amax = 0.0f;
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+          amax = fmaxf(amax, fmaxf(fabsf(__uint_as_float(x[k] << 16)), fabsf(__uint_as_float(x[k] & 0xFFFF0000u))));
+#pragma unroll
+        for (int d = 1; d < LPR; d <<= 1) amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, d));
+        const int e = amax == 0.0f ? 0 : min(7 - floor_log2(amax), 126);
+        float f = exp2_int(e);
+        if (p.scale < 0.0f) f = -f;
+        if (!(amax <= 3.402823466e38f)) f = __int_as_float(0x7FFFFFFF);
+        if (c == 0) q_exp[qb][r] = (int8_t)e;
+        uint32_t hi[4], lo[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float x0 = __uint_as_float(x[2 * i] << 16) * f, x1 = __uint_as_float(x[2 * i] & 0xFFFF0000u) * f;
+          const float x2 = __uint_as_float(x[2 * i + 1] << 16) * f, x3 = __uint_as_float(x[2 * i + 1] & 0xFFFF0000u) * f;
+          hi[i] = encode4(x0, x1, x2, x3);
+          uint32_t d0, d1;
+          decode4(hi[i], d0, d1);
+          const float2 y0 = f16x2_to_f32(d0), y1 = f16x2_to_f32(d1);
+          lo[i] = encode4(x0 - y0.x, x1 - y0.y, x2 - y1.x, x3 - y1.y);
+        }
+        *reinterpret_cast<uint4*>(q8 + swizzled<D>(r, c)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+        *reinterpret_cast<uint4*>(q8 + kRows * D + swizzled<D>(r, c)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      ew_arrive(&q_full[qb]);
+      ++qn;
+    }
   } else {
-    // ------------------------------------------------------------ softmax, a row per thread
-    const uint32_t lane_tmem = tmem + ((uint32_t)(warp * 32) << 16);
+    // ------------------------------------------------------------ softmax
+    const int row = tid & 127, half = tid >> 7;  // half: the group, tiles of this parity
+    auto both = [] { asm volatile("bar.sync 1, 256;" ::: "memory"); };
+    const uint32_t lane_tmem = tmem + ((uint32_t)((warp & 3) * 32) << 16);
+    const uint32_t s_tmem = lane_tmem + half * kTile, o_tmem = lane_tmem + G::OCOL + half * D;
     bool first = true;
     while (it.next(p, group)) {
-      const int nt = it.nt, rr = it.row0 + tid, tok = rr / group;
-      const bool live = tid < it.nrows;
+      const int nt = it.nt, rr = it.row0 + row, tok = rr / group;
+      const bool live = row < it.nrows;
       const int64_t at = (int64_t)(it.rq.q0 + tok) * p.Hq + it.hk * group + rr - tok * group;
       if (first && tid == 0)
         p.cut[blockIdx.x] = {it.u0, it.span, it.rq.q0 * group + it.row0, it.hk, it.nrows, {0, 0, 0}};
       // keys that the row sees; that all of the tile's rows see
       const int lim = live ? min(it.rq.kv, it.rq.kv - it.rq.n + tok + 1) : 0;
       const int all_see = it.rq.kv - it.rq.n + it.row0 / group + 1;
-      // the row as 2^-e (q1 + q2), in the sign of the scale; not finite: a row of NaN
       float qs = 0.0f;
       if (nt > 0) {
-        const uint4* src = reinterpret_cast<const uint4*>(p.q + (int64_t)(it.rq.q0 + tok) * p.ld_q +
-                                                          (int64_t)(it.hk * group + rr - tok * group) * D);
-        float amax = 0.0f;
-        if (live) {
-#pragma unroll 4
-          for (int i = 0; i < D / 8; ++i) {
-            const uint4 w = src[i];
-            const uint32_t x[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-              amax = fmaxf(amax, fmaxf(fabsf(__uint_as_float(x[k] << 16)), fabsf(__uint_as_float(x[k] & 0xFFFF0000u))));
-          }
-        }
-        const int e = amax == 0.0f ? 0 : min(7 - floor_log2(amax), 126);
-        float f = exp2_int(e);
-        if (p.scale < 0.0f) f = -f;
-        if (!(amax <= 3.402823466e38f)) f = __int_as_float(0x7FFFFFFF);
+        wait(&q_full[qn & 1], (qn >> 1) & 1);
         // (a zero scale stays apart from a key that is not seen: -inf * qs)
-        qs = fmaxf(fabsf(p.scale) * 1.4426950408889634f * exp2_int(-e), 1.175494351e-38f);
-#pragma unroll 1
-        for (int c = 0; c < D / 16; ++c) {
-          uint32_t hi[4] = {}, lo[4] = {};
-          if (live) {
-            const uint4 v[2] = {src[2 * c], src[2 * c + 1]};
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const uint32_t a = i & 1 ? v[i >> 1].z : v[i >> 1].x, b = i & 1 ? v[i >> 1].w : v[i >> 1].y;
-              const float x0 = __uint_as_float(a << 16) * f, x1 = __uint_as_float(a & 0xFFFF0000u) * f;
-              const float x2 = __uint_as_float(b << 16) * f, x3 = __uint_as_float(b & 0xFFFF0000u) * f;
-              hi[i] = encode4(x0, x1, x2, x3);
-              uint32_t d0, d1;
-              decode4(hi[i], d0, d1);
-              const float2 y0 = f16x2_to_f32(d0), y1 = f16x2_to_f32(d1);
-              lo[i] = encode4(x0 - y0.x, x1 - y0.y, x2 - y1.x, x3 - y1.y);
-            }
-          }
-          *reinterpret_cast<uint4*>(smem + G::QOFF + swizzled<D>(tid, c)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-          *reinterpret_cast<uint4*>(smem + G::QOFF + kRows * D + swizzled<D>(tid, c)) =
-              make_uint4(lo[0], lo[1], lo[2], lo[3]);
-        }
-        fence_proxy_async_smem();
-        __syncwarp();
-        ew_arrive(&q_full);
+        qs = fmaxf(fabsf(p.scale) * 1.4426950408889634f * exp2_int(-q_exp[qn & 1][row]), 1.175494351e-38f);
       }
 
-      float m = -INFINITY, ref = 0.0f, l = 0.0f;  // reference (0 while there is none), sum
-      int unit = -127;  // outputs are in units of 2^unit, the largest value exponent so far
-      for (int i = 0; i < nt; ++i, ++gc) {
-        const int key0 = (it.t0 + i) * kTile, buf = gc & 1, hd = gc & (kHeads - 1);
-        wait(&s_full[buf], (gc >> 1) & 1);
+      float m = -INFINITY, ref = 0.0f, l = 0.0f;  // of the group: reference (0 while there is none), sum
+      int unit = -127;  // the group's outputs are in units of 2^unit, the largest value exponent so far
+      for (int i = (gc ^ half) & 1; i < nt; i += 2) {
+        const int n = gc + i, key0 = (it.t0 + i) * kTile, hd = n & (kHeads - 1);
+        wait(&s_full[half], (n >> 1) & 1);
         tc_fence_after();
-        wait(&heads.full[hd], gc / kHeads & 1);
+        wait(&heads.full[hd], n / kHeads & 1);
         const int2 vr = heads.vrange[hd];
         // the row's logits, 32 keys at a time, twice: for the maximum, then for the
         // weights.  Loops stay rolled: unrolled, the roles' code outgrew the
         // instruction cache, and half of all issue slots were lost to it.
-        const uint32_t s_tmem = lane_tmem + buf * kTile;
         const int seen = lim - key0;
         const bool odd = key0 + kTile > all_see || vr.x == kNoPage;
         auto hide = [&](uint32_t (&x)[32], int k) {  // keys that the row does not see are -inf
@@ -321,84 +320,107 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
           l *= f;
           m = m1;
           ref = r1;
-          if (i > 0) {
+          if (i > 1) {
             const float fo = f * exp2_int(max(unit - unit1, -127));
-            wait(&pv_done, (gc & 1) ^ 1);
+            wait(&pv_done[half], ((n >> 1) & 1) ^ 1);
             tc_fence_after();
 #pragma unroll 1
             for (int o = 0; o < D; o += 32) {
               uint32_t y[32];
-              tmem_ld_32x32b_x32(lane_tmem + G::OCOL + o, y);
+              tmem_ld_32x32b_x32(o_tmem + o, y);
               tmem_ld_wait();
 #pragma unroll
               for (int j = 0; j < 32; ++j) y[j] = __float_as_uint(__uint_as_float(y[j]) * fo);
-              tmem_st_32x32b_x32(lane_tmem + G::OCOL + o, y);
+              tmem_st_32x32b_x32(o_tmem + o, y);
             }
-            tmem_st_wait();
-            tc_fence_before();
           }
           unit = unit1;
         }
-        const float up = kRowBoost - ref;
-        float sum[4] = {};
-        wait(&pv_done, (gc & 1) ^ 1);  // the last product has read P
+        // weights over the logits, times their values' power of two
 #pragma unroll 1
         for (int k = 0; k < kTile; k += 32) {
-          uint32_t x[32];
+          uint32_t x[32], w[16];
           tmem_ld_32x32b_x32(s_tmem + k, x);
-          const float c0 = factor(k), c1 = factor(k + 16);
+          const float c[2] = {factor(k), factor(k + 16)};
+          int ve[2];
+#pragma unroll
+          for (int h = 0; h < 2; ++h) ve[h] = max(heads.vexp[hd][(k + 16 * h) >> p.shift] - unit, kFarExp);
           tmem_ld_wait();
           if (odd) hide(x, k);
-          uint8_t* dst = smem + G::POFF + (k >> 6) * (kRows * 128);
 #pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            uint32_t w[4];
+          for (int h = 0; h < 2; ++h) {
+            const float up = kRowBoost - ref + (float)ve[h];
+            const uint64_t cc = pack2(c[h], c[h]), uu = pack2(up, up);
+            uint64_t sum[2] = {0, 0};
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              const int n = 8 * q + 2 * j;
-              const float a = ex2(fmaf(__uint_as_float(x[n]), q < 2 ? c0 : c1, up));
-              const float b = ex2(fmaf(__uint_as_float(x[n + 1]), q < 2 ? c0 : c1, up));
-              sum[j] += a + b;
-              const __half2 h = __floats2half2_rn(a, b);
-              w[j] = *reinterpret_cast<const uint32_t*>(&h);
+            for (int j = 0; j < 8; ++j) {
+              const int e = 16 * h + 2 * j;
+              float2 y = unpack2(fma2(pack2(__uint_as_float(x[e]), __uint_as_float(x[e + 1])), cc, uu));
+              y.x = ex2(y.x);
+              y.y = ex2(y.y);
+              sum[j & 1] = add2(sum[j & 1], pack2(y.x, y.y));
+              const __half2 z = __floats2half2_rn(y.x, y.y);
+              w[8 * h + j] = *reinterpret_cast<const uint32_t*>(&z);
             }
-            *reinterpret_cast<uint4*>(dst + swizzled<128>(tid, (k >> 3 & 4) + q)) = make_uint4(w[0], w[1], w[2], w[3]);
+            const float2 y = unpack2(add2(sum[0], sum[1]));
+            l = fmaf(y.x + y.y, exp2_int(-ve[h]), l);
           }
+          tmem_st16(s_tmem + (k >> 1), w);
         }
+        tmem_st_wait();
         tc_fence_before();
         __syncwarp();
-        ew_arrive(&s_empty[buf]);
-        l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-        fence_proxy_async_smem();
-        __syncwarp();
-        ew_arrive(&p_full);
+        ew_arrive(&p_full[half]);
       }
 
-      // ---- the piece's result
-      const bool whole = it.take == it.span, none = l == 0.0f;
-      const int64_t part = ((int64_t)blockIdx.x * 2 + (first ? 0 : 1)) * kRows + tid;
-      const float inv = none ? 0.0f : reciprocal(l), us = exp2_int(unit);
-      const float lse2 = none ? -INFINITY : ref + (lg2(l) - kRowBoost);
-      if (live) {
+      // ---- the piece's result: both groups' parts, half of the columns each
+      const bool whole = it.take == it.span;
+      const int64_t part = ((int64_t)blockIdx.x * 2 + (first ? 0 : 1)) * kRows + row;
+      const int g0 = gc & 1;  // the group that has its first tile
+      bool none = true;
+      float f[2] = {0.0f, 0.0f}, us[2] = {1.0f, 1.0f}, lse2 = -INFINITY;
+      gc += nt;
+      if (nt > 0) {
+        both();  // all of S is there, and Q's buffer free
+        float4* stats = reinterpret_cast<float4*>(smem + G::QOFF + (qn & 1) * (2 * kRows * D));
+        stats[half * kRows + row] = make_float4(l == 0.0f ? -INFINITY : ref, l, exp2_int(unit), 0.0f);
+        both();
+        const float4 a = stats[row], b = stats[kRows + row];
+        __syncwarp();
+        ew_arrive(&q_empty[qn & 1]);
+        ++qn;
+        const float top = fmaxf(a.x, b.x), wa = ex2(a.x - top), wb = ex2(b.x - top);
+        const float sum = (a.x == -INFINITY ? 0.0f : a.y * wa) + (b.x == -INFINITY ? 0.0f : b.y * wb);
+        none = sum == 0.0f;
+        if (!none) {
+          const float inv = reciprocal(sum);
+          f[0] = wa * inv, f[1] = wb * inv;
+          us[0] = a.z, us[1] = b.z;
+          lse2 = top + (lg2(sum) - kRowBoost);
+        }
+        const int last = gc - 1;  // its group has the last tile, the other group the one before
+        wait(&pv_done[last & 1], (last >> 1) & 1);
+        if (nt > 1) wait(&pv_done[(last & 1) ^ 1], ((last - 1) >> 1) & 1);
+        tc_fence_after();
+      }
+      if (live && half == 0) {
         if (!whole) p.part_lse[part] = lse2;
         else if (p.lse != nullptr) p.lse[at] = lse2 * 0.6931471805599453f;
       }
-      if (nt > 0) {
-        wait(&pv_done, (gc & 1) ^ 1);
-        tc_fence_after();
-      }
 #pragma unroll 1
-      for (int o = 0; o < D; o += 32) {
-        uint32_t x[32];
-        if (nt > 0) {
-          tmem_ld_32x32b_x32(lane_tmem + G::OCOL + o, x);
+      for (int o = half * (D / 2); o < (half + 1) * (D / 2); o += 32) {
+        float y[32] = {};
+#pragma unroll 1
+        for (int i = 0; i < min(nt, 2); ++i) {
+          const int g = g0 ^ i;
+          uint32_t x[32];
+          tmem_ld_32x32b_x32(lane_tmem + G::OCOL + g * D + o, x);
           tmem_ld_wait();
-        }
-        float y[32];
+          const float fg = g ? f[1] : f[0], ug = g ? us[1] : us[0];
 #pragma unroll
-        for (int j = 0; j < 32; ++j) y[j] = none ? 0.0f : __uint_as_float(x[j]) * inv * us;
-        if (!live) continue;
-        if (whole) {
+          for (int j = 0; j < 32; ++j) y[j] += none ? 0.0f : __uint_as_float(x[j]) * fg * ug;
+        }
+        if (live && whole) {
           uint32_t w[16];
 #pragma unroll
           for (int j = 0; j < 16; ++j) {
@@ -408,20 +430,22 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
           uint4* dst = reinterpret_cast<uint4*>(p.out + at * D + o);
 #pragma unroll
           for (int j = 0; j < 4; ++j) dst[j] = make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
-        } else {
+        } else if (live) {
           float4* dst = reinterpret_cast<float4*>(p.part + part * D + o);
 #pragma unroll
           for (int j = 0; j < 8; ++j) dst[j] = make_float4(y[4 * j], y[4 * j + 1], y[4 * j + 2], y[4 * j + 3]);
         }
+        __syncwarp();
       }
       tc_fence_before();
+      both();  // (both groups' outputs are read)
       first = false;
     }
     if (first && tid == 0) p.cut[blockIdx.x].before = 0;
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == 5) {
+  if (warp == 9) {
     tc_fence_after();
     tmem_dealloc(tmem, G::COLS);
   }
