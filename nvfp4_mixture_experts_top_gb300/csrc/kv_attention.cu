@@ -151,7 +151,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
   bool ok = true;
   int gc = 0;  // tiles of the CTA so far, the same count in every role
   if (warp == 4) {
-    copy_tiles<D, SUBS, R>(p, group, it, &tm_k, &tm_v, smem + G::ROFF, full, empty, heads, &abort_flag);
+    copy_tiles<D, SUBS>(p, group, it, &tm_k, &tm_v, smem + G::ROFF, full, empty, heads, &abort_flag);
   } else if (warp == 5) {
     // ------------------------------------------------------------ products
     constexpr uint32_t idesc_s = idesc_e4m3(128, NS, false), idesc_o = idesc_e4m3(128, NP, true) | (1u << 10);  // P is E5M2

@@ -140,18 +140,21 @@ struct Work {
   }
 };
 
-// Walks the pieces of sequences that a range of the work consists of.  A cut inside a
-// tile falls on the tile's start, one inside the cost before its first tile.
-template <int R>
-struct Pieces {
+// Of a sequence, the part in one CTA's range.
+struct Piece {
   int b;         // request
-  int64_t off;   // work of the request before the position
-  int64_t left;  // work of the range after the position
-  // the current piece
   Request rq;
   int hk, row0, nrows, span, u0, take;
   int limit;     // keys that the last row of the tile sees
   int t0, nt;    // its tiles
+};
+
+// Walks the pieces of sequences that a range of the work consists of.  A cut inside a
+// tile falls on the tile's start, one inside the cost before its first tile.
+template <int R>
+struct Pieces : Piece {
+  int64_t off;   // work of the request before the position
+  int64_t left;  // work of the range after the position
 
   __device__ __forceinline__ bool next(const Params& p, int group) {
     if (left <= 0) return false;
@@ -277,8 +280,8 @@ struct Heads {
 
 // The copying warp: K and V of the range's tiles in turn through a ring of SUBS
 // slots of kTile * D bytes, page by page.
-template <int D, int SUBS, int R>
-__device__ __forceinline__ void copy_tiles(const Params& p, int group, Pieces<R>& it, const CUtensorMap* tm_k,
+template <int D, int SUBS, typename It>
+__device__ __forceinline__ void copy_tiles(const Params& p, int group, It& it, const CUtensorMap* tm_k,
                                            const CUtensorMap* tm_v, uint8_t* ring, uint64_t* full, uint64_t* empty,
                                            Heads& heads, volatile int* abort_flag) {
   const int lane = threadIdx.x & 31;
@@ -347,7 +350,7 @@ __device__ __forceinline__ void copy_tiles(const Params& p, int group, Pieces<R>
       ew_arrive(&heads.full[gc & (kHeads - 1)]);
     }
   }
-  if (!ok) {  // given up: no copy may outlive the CTA's memory
+  if (!ok || *abort_flag) {  // given up: no copy may outlive the CTA's memory
     for (int i = 0; i < SUBS; ++i)
       if (issued >> i & 1) mbar_wait(&full[i], issued_par >> i & 1);
   }

@@ -42,6 +42,24 @@ struct Geo {
   static constexpr int COLS = 512;
 };
 
+// The pieces as the query rows' warps pass them on with the rows, for a role that
+// keeps what it needs in registers: the entry is given back at once.
+struct Feed : Piece {
+  const Piece* at;
+  uint64_t *full, *empty;
+  volatile int* abort_flag;
+  int32_t* dev_status;
+  int n;
+  __device__ __forceinline__ bool next(const Params&, int) {
+    if (!warp_wait(&full[n & 1], (n >> 1) & 1, abort_flag, dev_status)) return false;
+    static_cast<Piece&>(*this) = at[n & 1];
+    __syncwarp();
+    ew_arrive(&empty[n & 1]);
+    ++n;
+    return nt >= 0;
+  }
+};
+
 template <int D>
 __global__ void __launch_bounds__(kPromptThreads, 1)
     kv_prompt_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
@@ -50,10 +68,11 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
   constexpr int SUBS = G::SUBS;
   extern __shared__ __align__(1024) uint8_t smem[];
   __shared__ __align__(8) uint64_t full[SUBS], empty[SUBS], s_full[2], p_full[2], pv_done[2], v_full[2], q_full[2],
-      q_empty[2], drained;
+      q_empty[2], pair, drained;
   __shared__ Heads heads;
   __shared__ RangeScratch<kPromptThreads> scratch;
   __shared__ int8_t q_exp[2][kRows];
+  __shared__ Piece pieces[2];
   __shared__ uint32_t tmem_s;
   __shared__ volatile int abort_flag;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -70,8 +89,9 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
       mbar_init(&pv_done[i], 1);
       mbar_init(&v_full[i], 4);
       mbar_init(&q_full[i], 2);
-      mbar_init(&q_empty[i], 8);
+      mbar_init(&q_empty[i], 14);  // softmax, V to f16, products, copies
     }
+    mbar_init(&pair, 8);
     mbar_init(&drained, 1);
     abort_flag = 0;
     fence_mbar_init();
@@ -88,18 +108,24 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
   pdl_wait();
   pdl_trigger();  // after this CTA's TMEM allocation
   const uint32_t tmem = tmem_s;
-  Pieces<kRows> it;
+  Pieces<kRows> it;  // (the query rows' warps go by it, the others by what these pass on)
   range_of_cta<kPromptThreads, kRows>(p, group, it, scratch);
+  Feed feed;
+  feed.at = pieces;
+  feed.full = q_full;
+  feed.empty = q_empty;
+  feed.abort_flag = &abort_flag;
+  feed.dev_status = p.dev_status;
+  feed.n = 0;
 
   bool ok = true;
-  int gc = 0, qn = 0;  // tiles and pieces of the CTA so far, the same counts in every role
+  int gc = 0;  // tiles of the CTA so far, the same count in every role
   auto wait = [&](uint64_t* bar, uint32_t parity) {
-    // (after a failure the softmax warps go on without waiting)
     if (ok) ok = warp_wait(bar, parity, &abort_flag, p.dev_status);
     return ok;
   };
   if (warp == 8) {
-    copy_tiles<D, SUBS, kRows>(p, group, it, &tm_k, &tm_v, smem + G::ROFF, full, empty, heads, &abort_flag);
+    copy_tiles<D, SUBS>(p, group, feed, &tm_k, &tm_v, smem + G::ROFF, full, empty, heads, &abort_flag);
   } else if (warp == 9) {
     // ------------------------------------------------------------ products
     constexpr uint32_t idesc_s = idesc_e4m3(kRows, kTile, false);
@@ -113,13 +139,12 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
     auto product_s = [&](int n) {  // S of tile n of the CTA, over the weights of tile n - 2
       if (!wait(&full[sub], phase) || !wait(&pv_done[n & 1], ((n >> 1) & 1) ^ 1)) return;
       tc_fence_after();
-      const uint32_t q = base + G::QOFF + (qn & 1) * (2 * kRows * D);
-#pragma unroll
-      for (int t = 0; t < 2; ++t)
-#pragma unroll
-        for (int k = 0; k < D / 32; ++k)
-          ew_mma_e4m3(tmem + (n & 1) * kTile, smem_desc(q + t * kRows * D + k * 32, 16, 8 * D, layout),
-                      smem_desc(ring + sub * kTile * D + k * 32, 16, 8 * D, layout), idesc_s, t > 0 || k > 0);
+      uint64_t q = smem_desc(base + G::QOFF + ((feed.n - 1) & 1) * (2 * kRows * D), 16, 8 * D, layout);
+      const uint64_t keys = smem_desc(ring + sub * kTile * D, 16, 8 * D, layout);
+#pragma unroll 1
+      for (int t = 0; t < 2; ++t, q += kRows * D / 16)
+#pragma unroll 1
+        for (int k = 0; k < D / 16; k += 2) ew_mma_e4m3(tmem + (n & 1) * kTile, q + k, keys + k, idesc_s, t | k);
       ew_commit(&empty[sub]);
       ew_commit(&s_full[n & 1]);
       issued = true;
@@ -129,27 +154,24 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
         phase ^= 1;
       }
     };
-    while (ok && it.next(p, group)) {
-      const int nt = it.nt;
+    while (ok && feed.next(p, group)) {
+      const int nt = feed.nt;
       if (nt == 0) continue;
-      if (!wait(&q_full[qn & 1], (qn >> 1) & 1)) break;
       product_s(gc);
       if (nt > 1) product_s(gc + 1);
       for (int i = 0; i < nt && ok; ++i, ++gc) {
         const int g = gc & 1;
         if (!wait(&v_full[g], (gc >> 1) & 1) || !wait(&p_full[g], (gc >> 1) & 1)) break;
         tc_fence_after();
-#pragma unroll
+        const uint64_t values = smem_desc(base + G::VOFF + g * (kTile * D * 2), kTile * 128, 1024, 2);
+#pragma unroll 1
         for (int k = 0; k < kTile / 16; ++k)
-          ew_mma_bf16_ts(tmem + G::OCOL + g * D, tmem + g * kTile + k * 8,
-                         smem_desc(base + G::VOFF + g * (kTile * D * 2) + k * 2048, kTile * 128, 1024, 2), idesc_o,
-                         i > 1 || k > 0);
+          ew_mma_bf16_ts(tmem + G::OCOL + g * D, tmem + g * kTile + k * 8, values + k * 128, idesc_o, i > 1 || k > 0);
         ew_commit(&pv_done[g]);
         if (i + 2 < nt) product_s(gc + 2);
       }
-      ++qn;
     }
-    if (!ok && issued) {  // given up: no product may outlive the operands and the TMEM
+    if (issued && (!ok || abort_flag)) {  // given up: no product may outlive the operands and the TMEM
       ew_commit(&drained);
       mbar_wait(&drained, 0);
     }
@@ -161,14 +183,14 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
     const int r0 = (D == 128 ? w >> 1 : w) * 8 + ((lane >> 3) ^ (lane & 4 ? 5 : 0));
     int sub = 1;
     uint32_t phase = 0;
-    while (it.next(p, group)) {
-      for (int i = 0; i < it.nt; ++i, ++gc) {
-        const int key0 = (it.t0 + i) * kTile, hd = gc & (kHeads - 1), g = gc & 1;
-        wait(&full[sub], phase);
-        wait(&heads.full[hd], gc / kHeads & 1);
-        wait(&pv_done[g], ((gc >> 1) & 1) ^ 1);
+    while (ok && feed.next(p, group)) {
+      for (int i = 0; i < feed.nt; ++i, ++gc) {
+        const int key0 = (feed.t0 + i) * kTile, hd = gc & (kHeads - 1), g = gc & 1;
+        if (!wait(&full[sub], phase) || !wait(&heads.full[hd], gc / kHeads & 1) ||
+            !wait(&pv_done[g], ((gc >> 1) & 1) ^ 1))
+          break;
         // rows past the sequence hold anything, and 0 * NaN would spread: zeros instead
-        const bool odd = key0 + kTile > it.limit || heads.vrange[hd].x == kNoPage;
+        const bool odd = key0 + kTile > feed.limit || heads.vrange[hd].x == kNoPage;
         const uint8_t* src = smem + G::ROFF + sub * kTile * D + swizzled<D>(r0, c);
         uint8_t* dst = smem + G::VOFF + g * (kTile * D * 2) + (c >> 2) * (kTile * 128);
         uint8_t* dst0 = dst + swizzled<128>(r0, (c & 3) * 2);
@@ -177,7 +199,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
 #pragma unroll 4
         for (int n = 0; n < kTile; n += STEP) {
           uint4 x = *reinterpret_cast<const uint4*>(src + n * D);
-          if (odd && (key0 + r0 + n >= it.limit || heads.vexp[hd][(r0 + n) >> p.shift] == kNoPage))
+          if (odd && (key0 + r0 + n >= feed.limit || heads.vexp[hd][(r0 + n) >> p.shift] == kNoPage))
             x = make_uint4(0, 0, 0, 0);
           uint32_t h[8];
           decode4(x.x, h[0], h[1]);
@@ -204,61 +226,87 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
     // that is not finite becomes NaN
     constexpr int LPR = D / 16;
     const int t = tid - 10 * 32, c = t % LPR;
-    while (it.next(p, group)) {
-      if (it.nt == 0) continue;
+    for (int qn = 0;; ++qn) {
+      const bool more = it.next(p, group);
       const int qb = qn & 1;
-      wait(&q_empty[qb], ((qn >> 1) & 1) ^ 1);
+      if (!wait(&q_empty[qb], ((qn >> 1) & 1) ^ 1)) break;
+      if (t == 0) {
+        pieces[qb] = it;
+        if (!more) pieces[qb].nt = -1;
+      }
       uint8_t* q8 = smem + G::QOFF + qb * (2 * kRows * D);
-#pragma unroll 2
-      for (int r = t / LPR; r < kRows; r += 64 / LPR) {
-        uint4 w[2] = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
-        if (r < it.nrows) {
-          const int qr = it.row0 + r, qt = qr / group;
-          const uint4* src = reinterpret_cast<const uint4*>(p.q + (int64_t)(it.rq.q0 + qt) * p.ld_q +
-                                                            (int64_t)(it.hk * group + qr - qt * group) * D + 16 * c);
-          w[0] = src[0];
-          w[1] = src[1];
+      const int rows = more && it.nt > 0 ? kRows : 0;
+      constexpr int UR = 4;  // loads in flight
+#pragma unroll 1
+      for (int r0 = t / LPR; r0 < rows; r0 += UR * (64 / LPR)) {
+        uint4 w[UR][2];
+#pragma unroll
+        for (int u = 0; u < UR; ++u) {
+          const int r = r0 + u * (64 / LPR);
+          w[u][0] = w[u][1] = make_uint4(0, 0, 0, 0);
+          if (r < it.nrows) {
+            const int qr = it.row0 + r, qt = qr / group;
+            const uint4* src = reinterpret_cast<const uint4*>(p.q + (int64_t)(it.rq.q0 + qt) * p.ld_q +
+                                                              (int64_t)(it.hk * group + qr - qt * group) * D + 16 * c);
+            w[u][0] = src[0];
+            w[u][1] = src[1];
+          }
         }
-        const uint32_t x[8] = {w[0].x, w[0].y, w[0].z, w[0].w, w[1].x, w[1].y, w[1].z, w[1].w};
-        float amax = 0.0f;
 #pragma unroll
-        for (int k = 0; k < 8; ++k)
-          amax = fmaxf(amax, fmaxf(fabsf(__uint_as_float(x[k] << 16)), fabsf(__uint_as_float(x[k] & 0xFFFF0000u))));
+        for (int u = 0; u < UR; ++u) {
+          const int r = r0 + u * (64 / LPR);
+          const uint32_t x[8] = {w[u][0].x, w[u][0].y, w[u][0].z, w[u][0].w, w[u][1].x, w[u][1].y, w[u][1].z, w[u][1].w};
+          float amax = 0.0f;
 #pragma unroll
-        for (int d = 1; d < LPR; d <<= 1) amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, d));
-        const int e = amax == 0.0f ? 0 : min(7 - floor_log2(amax), 126);
-        float f = exp2_int(e);
-        if (p.scale < 0.0f) f = -f;
-        if (!(amax <= 3.402823466e38f)) f = __int_as_float(0x7FFFFFFF);
-        if (c == 0) q_exp[qb][r] = (int8_t)e;
-        uint32_t hi[4], lo[4];
+          for (int k = 0; k < 8; ++k)
+            amax = fmaxf(amax, fmaxf(fabsf(__uint_as_float(x[k] << 16)), fabsf(__uint_as_float(x[k] & 0xFFFF0000u))));
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float x0 = __uint_as_float(x[2 * i] << 16) * f, x1 = __uint_as_float(x[2 * i] & 0xFFFF0000u) * f;
-          const float x2 = __uint_as_float(x[2 * i + 1] << 16) * f, x3 = __uint_as_float(x[2 * i + 1] & 0xFFFF0000u) * f;
-          hi[i] = encode4(x0, x1, x2, x3);
-          uint32_t d0, d1;
-          decode4(hi[i], d0, d1);
-          const float2 y0 = f16x2_to_f32(d0), y1 = f16x2_to_f32(d1);
-          lo[i] = encode4(x0 - y0.x, x1 - y0.y, x2 - y1.x, x3 - y1.y);
+          for (int d = 1; d < LPR; d <<= 1) amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, d));
+          const int e = amax == 0.0f ? 0 : min(7 - floor_log2(amax), 126);
+          float f = exp2_int(e);
+          if (p.scale < 0.0f) f = -f;
+          if (!(amax <= 3.402823466e38f)) f = __int_as_float(0x7FFFFFFF);
+          if (c == 0) q_exp[qb][r] = (int8_t)e;
+          uint32_t hi[4], lo[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float x0 = __uint_as_float(x[2 * i] << 16) * f, x1 = __uint_as_float(x[2 * i] & 0xFFFF0000u) * f;
+            const float x2 = __uint_as_float(x[2 * i + 1] << 16) * f,
+                        x3 = __uint_as_float(x[2 * i + 1] & 0xFFFF0000u) * f;
+            hi[i] = encode4(x0, x1, x2, x3);
+            uint32_t d0, d1;
+            decode4(hi[i], d0, d1);
+            const float2 y0 = f16x2_to_f32(d0), y1 = f16x2_to_f32(d1);
+            lo[i] = encode4(x0 - y0.x, x1 - y0.y, x2 - y1.x, x3 - y1.y);
+          }
+          *reinterpret_cast<uint4*>(q8 + swizzled<D>(r, c)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+          *reinterpret_cast<uint4*>(q8 + kRows * D + swizzled<D>(r, c)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
         }
-        *reinterpret_cast<uint4*>(q8 + swizzled<D>(r, c)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-        *reinterpret_cast<uint4*>(q8 + kRows * D + swizzled<D>(r, c)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
       }
       fence_proxy_async_smem();
       __syncwarp();
       ew_arrive(&q_full[qb]);
-      ++qn;
+      if (!more) break;
     }
   } else {
     // ------------------------------------------------------------ softmax
     const int row = tid & 127, half = tid >> 7;  // half: the group, tiles of this parity
-    auto both = [] { asm volatile("bar.sync 1, 256;" ::: "memory"); };
+    uint32_t pair_phase = 0;
+    auto both = [&] {  // both groups are here
+      __syncwarp();
+      ew_arrive(&pair);
+      wait(&pair, pair_phase);
+      pair_phase ^= 1;
+      return ok;
+    };
     const uint32_t lane_tmem = tmem + ((uint32_t)((warp & 3) * 32) << 16);
     const uint32_t s_tmem = lane_tmem + half * kTile, o_tmem = lane_tmem + G::OCOL + half * D;
     bool first = true;
-    while (it.next(p, group)) {
+    for (int qn = 0; wait(&q_full[qn & 1], (qn >> 1) & 1); ++qn) {
+      const int qb = qn & 1;
+      const Piece it = pieces[qb];
       const int nt = it.nt, rr = it.row0 + row, tok = rr / group;
+      if (nt < 0) break;
       const bool live = row < it.nrows;
       const int64_t at = (int64_t)(it.rq.q0 + tok) * p.Hq + it.hk * group + rr - tok * group;
       if (first && tid == 0)
@@ -266,33 +314,35 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
       // keys that the row sees; that all of the tile's rows see
       const int lim = live ? min(it.rq.kv, it.rq.kv - it.rq.n + tok + 1) : 0;
       const int all_see = it.rq.kv - it.rq.n + it.row0 / group + 1;
-      float qs = 0.0f;
-      if (nt > 0) {
-        wait(&q_full[qn & 1], (qn >> 1) & 1);
-        // (a zero scale stays apart from a key that is not seen: -inf * qs)
-        qs = fmaxf(fabsf(p.scale) * 1.4426950408889634f * exp2_int(-q_exp[qn & 1][row]), 1.175494351e-38f);
-      }
+      // (a zero scale stays apart from a key that is not seen: -inf * qs)
+      const float qs = fmaxf(fabsf(p.scale) * 1.4426950408889634f * exp2_int(-q_exp[qb][row]), 1.175494351e-38f);
 
       float m = -INFINITY, ref = 0.0f, l = 0.0f;  // of the group: reference (0 while there is none), sum
       int unit = -127;  // the group's outputs are in units of 2^unit, the largest value exponent so far
       for (int i = (gc ^ half) & 1; i < nt; i += 2) {
         const int n = gc + i, key0 = (it.t0 + i) * kTile, hd = n & (kHeads - 1);
-        wait(&s_full[half], (n >> 1) & 1);
+        if (!wait(&s_full[half], (n >> 1) & 1) || !wait(&heads.full[hd], n / kHeads & 1)) break;
         tc_fence_after();
-        wait(&heads.full[hd], n / kHeads & 1);
         const int2 vr = heads.vrange[hd];
         // the row's logits, 32 keys at a time, twice: for the maximum, then for the
         // weights.  Loops stay rolled: unrolled, the roles' code outgrew the
         // instruction cache, and half of all issue slots were lost to it.
         const int seen = lim - key0;
         const bool odd = key0 + kTile > all_see || vr.x == kNoPage;
-        auto hide = [&](uint32_t (&x)[32], int k) {  // keys that the row does not see are -inf
-          const bool gone0 = heads.vexp[hd][k >> p.shift] == kNoPage;
-          const bool gone1 = heads.vexp[hd][(k + 16) >> p.shift] == kNoPage;
+        if (odd) {  // keys that the row does not see are -inf
+#pragma unroll 1
+          for (int k = 0; k < kTile; k += 16) {
+            uint32_t x[16];
+            tmem_ld16(s_tmem + k, x);
+            const int left = heads.vexp[hd][k >> p.shift] == kNoPage ? 0 : seen - k;
+            tmem_ld_wait();
 #pragma unroll
-          for (int j = 0; j < 32; ++j)
-            if (k + j >= seen || (j < 16 ? gone0 : gone1)) x[j] = 0xFF800000u;
-        };
+            for (int j = 0; j < 16; ++j)
+              if (j >= left) x[j] = 0xFF800000u;
+            tmem_st16(s_tmem + k, x);
+          }
+          tmem_st_wait();
+        }
         // log2 units per unit of S
         auto factor = [&](int k) {
           return fminf(fmaxf(qs * heads.kscale[hd][k >> p.shift], 1.175494351e-38f), 3.402823466e38f);
@@ -304,7 +354,6 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
           tmem_ld_32x32b_x32(s_tmem + k, x);
           const float c0 = factor(k), c1 = factor(k + 16);
           tmem_ld_wait();
-          if (odd) hide(x, k);
           float mx[8];
 #pragma unroll
           for (int j = 0; j < 8; ++j)
@@ -322,8 +371,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
           ref = r1;
           if (i > 1) {
             const float fo = f * exp2_int(max(unit - unit1, -127));
-            wait(&pv_done[half], ((n >> 1) & 1) ^ 1);
-            tc_fence_after();
+            // (S of this tile came after the product before)
 #pragma unroll 1
             for (int o = 0; o < D; o += 32) {
               uint32_t y[32];
@@ -346,7 +394,6 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
 #pragma unroll
           for (int h = 0; h < 2; ++h) ve[h] = max(heads.vexp[hd][(k + 16 * h) >> p.shift] - unit, kFarExp);
           tmem_ld_wait();
-          if (odd) hide(x, k);
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
             const float up = kRowBoost - ref + (float)ve[h];
@@ -380,15 +427,17 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
       bool none = true;
       float f[2] = {0.0f, 0.0f}, us[2] = {1.0f, 1.0f}, lse2 = -INFINITY;
       gc += nt;
-      if (nt > 0) {
-        both();  // all of S is there, and Q's buffer free
-        float4* stats = reinterpret_cast<float4*>(smem + G::QOFF + (qn & 1) * (2 * kRows * D));
+      if (nt == 0) {
+        __syncwarp();
+        ew_arrive(&q_empty[qb]);
+      } else {
+        if (!both()) break;  // all of S is there, and Q's buffer free
+        float4* stats = reinterpret_cast<float4*>(smem + G::QOFF + qb * (2 * kRows * D));
         stats[half * kRows + row] = make_float4(l == 0.0f ? -INFINITY : ref, l, exp2_int(unit), 0.0f);
-        both();
+        if (!both()) break;
         const float4 a = stats[row], b = stats[kRows + row];
         __syncwarp();
-        ew_arrive(&q_empty[qn & 1]);
-        ++qn;
+        ew_arrive(&q_empty[qb]);
         const float top = fmaxf(a.x, b.x), wa = ex2(a.x - top), wb = ex2(b.x - top);
         const float sum = (a.x == -INFINITY ? 0.0f : a.y * wa) + (b.x == -INFINITY ? 0.0f : b.y * wb);
         none = sum == 0.0f;
@@ -399,8 +448,8 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
           lse2 = top + (lg2(sum) - kRowBoost);
         }
         const int last = gc - 1;  // its group has the last tile, the other group the one before
-        wait(&pv_done[last & 1], (last >> 1) & 1);
-        if (nt > 1) wait(&pv_done[(last & 1) ^ 1], ((last - 1) >> 1) & 1);
+        if (!wait(&pv_done[last & 1], (last >> 1) & 1)) break;
+        if (nt > 1 && !wait(&pv_done[(last & 1) ^ 1], ((last - 1) >> 1) & 1)) break;
         tc_fence_after();
       }
       if (live && half == 0) {
@@ -437,9 +486,9 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
         }
         __syncwarp();
       }
-      tc_fence_before();
-      both();  // (both groups' outputs are read)
       first = false;
+      tc_fence_before();
+      if (!both()) break;  // (both groups' outputs are read)
     }
     if (first && tid == 0) p.cut[blockIdx.x].before = 0;
   }
