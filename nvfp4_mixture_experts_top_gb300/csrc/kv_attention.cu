@@ -161,7 +161,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
     uint32_t phase = 0, q_phase = 0;
     bool issued = false;
     auto wait = [&](uint64_t* bar, uint32_t parity) {
-      if (ok) ok = warp_wait(bar, parity, &abort_flag, p.dev_status);
+      if (ok) ok = lean_wait(bar, parity, &abort_flag, p.dev_status);
       return ok;
     };
     auto advance = [&] {
@@ -225,7 +225,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
     // ------------------------------------------------------------ softmax
     auto wait = [&](uint64_t* bar, uint32_t parity) {
       // after a failure the warps go on without waiting, so that they still meet at their barriers
-      if (ok) ok = warp_wait(bar, parity, &abort_flag, p.dev_status);
+      if (ok) ok = lean_wait(bar, parity, &abort_flag, p.dev_status);
     };
     const uint32_t lane_tmem = tmem + ((uint32_t)(warp * 32) << 16);
     // query rows, a thread per 16 elements; asked for one piece ahead

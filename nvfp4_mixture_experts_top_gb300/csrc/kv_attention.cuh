@@ -269,6 +269,17 @@ __device__ __forceinline__ void range_of_cta(const Params& p, int group, Pieces<
   }
 }
 
+// warp_wait with the waiting out of line: inline it is fetched through at each wait,
+// and the attention kernels are short of instruction fetch (three 2K chunks: 364 -> 348 us).
+__device__ __noinline__ static bool wait_on(uint64_t* bar, uint32_t parity, volatile int* abort_flag,
+                                            int32_t* dev_status) {
+  return warp_wait(bar, parity, abort_flag, dev_status);
+}
+__device__ __forceinline__ bool lean_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag,
+                                          int32_t* dev_status) {
+  return __all_sync(0xFFFFFFFFu, mbar_try_wait(bar, parity)) || wait_on(bar, parity, abort_flag, dev_status);
+}
+
 // What the copying warp says of a tile: scale and exponent of its pages, and the
 // smallest (kNoPage: some page is missing) and largest exponent.
 struct Heads {
@@ -319,7 +330,7 @@ __device__ __forceinline__ void copy_tiles(const Params& p, int group, It& it, c
       const bool mine = lane >= j && lane < j + per_tile;
       const uint32_t here = __popc(__ballot_sync(0xFFFFFFFFu, mine && page >= 0)) * page_bytes;
       for (int h = 0; h < 2 && ok; ++h) {
-        if (!warp_wait(&empty[sub], phase, abort_flag, p.dev_status)) {
+        if (!lean_wait(&empty[sub], phase, abort_flag, p.dev_status)) {
           ok = false;
           break;
         }

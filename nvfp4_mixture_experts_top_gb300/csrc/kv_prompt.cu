@@ -51,7 +51,7 @@ struct Feed : Piece {
   int32_t* dev_status;
   int n;
   __device__ __forceinline__ bool next(const Params&, int) {
-    if (!warp_wait(&full[n & 1], (n >> 1) & 1, abort_flag, dev_status)) return false;
+    if (!lean_wait(&full[n & 1], (n >> 1) & 1, abort_flag, dev_status)) return false;
     static_cast<Piece&>(*this) = at[n & 1];
     __syncwarp();
     ew_arrive(&empty[n & 1]);
@@ -85,7 +85,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
     for (int i = 0; i < kHeads; ++i) mbar_init(&heads.full[i], 1);
     for (int i = 0; i < 2; ++i) {
       mbar_init(&s_full[i], 1);
-      mbar_init(&p_full[i], 4);
+      mbar_init(&p_full[i], 8);
       mbar_init(&pv_done[i], 1);
       mbar_init(&v_full[i], 4);
       mbar_init(&q_full[i], 2);
@@ -121,7 +121,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
   bool ok = true;
   int gc = 0;  // tiles of the CTA so far, the same count in every role
   auto wait = [&](uint64_t* bar, uint32_t parity) {
-    if (ok) ok = warp_wait(bar, parity, &abort_flag, p.dev_status);
+    if (ok) ok = lean_wait(bar, parity, &abort_flag, p.dev_status);
     return ok;
   };
   if (warp == 8) {
@@ -166,7 +166,8 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
         const uint64_t values = smem_desc(base + G::VOFF + g * (kTile * D * 2), kTile * 128, 1024, 2);
 #pragma unroll 1
         for (int k = 0; k < kTile / 16; ++k)
-          ew_mma_bf16_ts(tmem + G::OCOL + g * D, tmem + g * kTile + k * 8, values + k * 128, idesc_o, i > 1 || k > 0);
+          ew_mma_bf16_ts(tmem + G::OCOL + (k >> 2) * D, tmem + g * kTile + (k >> 2) * 64 + (k & 3) * 8, values + k * 128,
+                         idesc_o, i > 0 || (k & 3) > 0);
         ew_commit(&pv_done[g]);
         if (i + 2 < nt) product_s(gc + 2);
       }
@@ -196,7 +197,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
         uint8_t* dst0 = dst + swizzled<128>(r0, (c & 3) * 2);
         uint8_t* dst1 = dst + swizzled<128>(r0, (c & 3) * 2 + 1);
         constexpr int STEP = D == 128 ? 16 : 32;
-#pragma unroll 4
+#pragma unroll 2
         for (int n = 0; n < kTile; n += STEP) {
           uint4 x = *reinterpret_cast<const uint4*>(src + n * D);
           if (odd && (key0 + r0 + n >= feed.limit || heads.vexp[hd][(r0 + n) >> p.shift] == kNoPage))
@@ -290,7 +291,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
     }
   } else {
     // ------------------------------------------------------------ softmax
-    const int row = tid & 127, half = tid >> 7;  // half: the group, tiles of this parity
+    const int row = tid & 127, half = tid >> 7;  // half: the group, of a tile's keys
     uint32_t pair_phase = 0;
     auto both = [&] {  // both groups are here
       __syncwarp();
@@ -300,7 +301,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
       return ok;
     };
     const uint32_t lane_tmem = tmem + ((uint32_t)((warp & 3) * 32) << 16);
-    const uint32_t s_tmem = lane_tmem + half * kTile, o_tmem = lane_tmem + G::OCOL + half * D;
+    const uint32_t o_tmem = lane_tmem + G::OCOL + half * D;
     bool first = true;
     for (int qn = 0; wait(&q_full[qn & 1], (qn >> 1) & 1); ++qn) {
       const int qb = qn & 1;
@@ -319,9 +320,10 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
 
       float m = -INFINITY, ref = 0.0f, l = 0.0f;  // of the group: reference (0 while there is none), sum
       int unit = -127;  // the group's outputs are in units of 2^unit, the largest value exponent so far
-      for (int i = (gc ^ half) & 1; i < nt; i += 2) {
-        const int n = gc + i, key0 = (it.t0 + i) * kTile, hd = n & (kHeads - 1);
-        if (!wait(&s_full[half], (n >> 1) & 1) || !wait(&heads.full[hd], n / kHeads & 1)) break;
+      for (int i = 0; i < nt; ++i, ++gc) {
+        const int key0 = (it.t0 + i) * kTile, hd = gc & (kHeads - 1), buf = gc & 1;
+        const uint32_t s_tmem = lane_tmem + buf * kTile;
+        if (!wait(&s_full[buf], (gc >> 1) & 1) || !wait(&heads.full[hd], gc / kHeads & 1)) break;
         tc_fence_after();
         const int2 vr = heads.vrange[hd];
         // the row's logits, 32 keys at a time, twice: for the maximum, then for the
@@ -331,7 +333,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
         const bool odd = key0 + kTile > all_see || vr.x == kNoPage;
         if (odd) {  // keys that the row does not see are -inf
 #pragma unroll 1
-          for (int k = 0; k < kTile; k += 16) {
+          for (int k = 64 * half; k < 64 * half + 64; k += 16) {
             uint32_t x[16];
             tmem_ld16(s_tmem + k, x);
             const int left = heads.vexp[hd][k >> p.shift] == kNoPage ? 0 : seen - k;
@@ -349,18 +351,17 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
         };
         float top = -INFINITY;
 #pragma unroll 1
-        for (int k = 0; k < kTile; k += 32) {
-          uint32_t x[32];
-          tmem_ld_32x32b_x32(s_tmem + k, x);
-          const float c0 = factor(k), c1 = factor(k + 16);
+        for (int k = 64 * half; k < 64 * half + 64; k += 16) {
+          uint32_t x[16];
+          tmem_ld16(s_tmem + k, x);
+          const float c0 = factor(k);
           tmem_ld_wait();
-          float mx[8];
+          float mx[4];
 #pragma unroll
-          for (int j = 0; j < 8; ++j)
+          for (int j = 0; j < 4; ++j)
             mx[j] = fmaxf(fmaxf(__uint_as_float(x[4 * j]), __uint_as_float(x[4 * j + 1])),
                           fmaxf(__uint_as_float(x[4 * j + 2]), __uint_as_float(x[4 * j + 3])));
-          top = fmaxf(top, fmaxf(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * c0,
-                                 fmaxf(fmaxf(mx[4], mx[5]), fmaxf(mx[6], mx[7])) * c1));
+          top = fmaxf(top, fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * c0);
         }
         const int unit1 = max(unit, vr.y);
         if (__any_sync(0xFFFFFFFFu, top > ref + kRowSlack || (m == -INFINITY && top != -INFINITY)) || unit1 != unit) {
@@ -369,9 +370,10 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
           l *= f;
           m = m1;
           ref = r1;
-          if (i > 1) {
+          if (i > 0) {
             const float fo = f * exp2_int(max(unit - unit1, -127));
-            // (S of this tile came after the product before)
+            if (!wait(&pv_done[buf ^ 1], ((gc - 1) >> 1) & 1)) break;
+            tc_fence_after();
 #pragma unroll 1
             for (int o = 0; o < D; o += 32) {
               uint32_t y[32];
@@ -386,47 +388,39 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
         }
         // weights over the logits, times their values' power of two
 #pragma unroll 1
-        for (int k = 0; k < kTile; k += 32) {
-          uint32_t x[32], w[16];
-          tmem_ld_32x32b_x32(s_tmem + k, x);
-          const float c[2] = {factor(k), factor(k + 16)};
-          int ve[2];
-#pragma unroll
-          for (int h = 0; h < 2; ++h) ve[h] = max(heads.vexp[hd][(k + 16 * h) >> p.shift] - unit, kFarExp);
+        for (int k = 64 * half; k < 64 * half + 64; k += 16) {
+          uint32_t x[16], w[8];
+          tmem_ld16(s_tmem + k, x);
+          const float c = factor(k);
+          const int ve = max(heads.vexp[hd][k >> p.shift] - unit, kFarExp);
+          const float up = kRowBoost - ref + (float)ve;
+          const uint64_t cc = pack2(c, c), uu = pack2(up, up);
           tmem_ld_wait();
+          uint64_t sum[2] = {0, 0};
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const float up = kRowBoost - ref + (float)ve[h];
-            const uint64_t cc = pack2(c[h], c[h]), uu = pack2(up, up);
-            uint64_t sum[2] = {0, 0};
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-              const int e = 16 * h + 2 * j;
-              float2 y = unpack2(fma2(pack2(__uint_as_float(x[e]), __uint_as_float(x[e + 1])), cc, uu));
-              y.x = ex2(y.x);
-              y.y = ex2(y.y);
-              sum[j & 1] = add2(sum[j & 1], pack2(y.x, y.y));
-              const __half2 z = __floats2half2_rn(y.x, y.y);
-              w[8 * h + j] = *reinterpret_cast<const uint32_t*>(&z);
-            }
-            const float2 y = unpack2(add2(sum[0], sum[1]));
-            l = fmaf(y.x + y.y, exp2_int(-ve[h]), l);
+          for (int j = 0; j < 8; ++j) {
+            float2 y = unpack2(fma2(pack2(__uint_as_float(x[2 * j]), __uint_as_float(x[2 * j + 1])), cc, uu));
+            y.x = ex2(y.x);
+            y.y = ex2(y.y);
+            sum[j & 1] = add2(sum[j & 1], pack2(y.x, y.y));
+            const __half2 z = __floats2half2_rn(y.x, y.y);
+            w[j] = *reinterpret_cast<const uint32_t*>(&z);
           }
-          tmem_st16(s_tmem + (k >> 1), w);
+          const float2 y = unpack2(add2(sum[0], sum[1]));
+          l = fmaf(y.x + y.y, exp2_int(-ve), l);
+          tmem_st8(s_tmem + 32 * half + (k >> 1), w);
         }
         tmem_st_wait();
         tc_fence_before();
         __syncwarp();
-        ew_arrive(&p_full[half]);
+        ew_arrive(&p_full[buf]);
       }
 
       // ---- the piece's result: both groups' parts, half of the columns each
       const bool whole = it.take == it.span;
       const int64_t part = ((int64_t)blockIdx.x * 2 + (first ? 0 : 1)) * kRows + row;
-      const int g0 = gc & 1;  // the group that has its first tile
       bool none = true;
       float f[2] = {0.0f, 0.0f}, us[2] = {1.0f, 1.0f}, lse2 = -INFINITY;
-      gc += nt;
       if (nt == 0) {
         __syncwarp();
         ew_arrive(&q_empty[qb]);
@@ -447,9 +441,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
           us[0] = a.z, us[1] = b.z;
           lse2 = top + (lg2(sum) - kRowBoost);
         }
-        const int last = gc - 1;  // its group has the last tile, the other group the one before
-        if (!wait(&pv_done[last & 1], (last >> 1) & 1)) break;
-        if (nt > 1 && !wait(&pv_done[(last & 1) ^ 1], ((last - 1) >> 1) & 1)) break;
+        if (!wait(&pv_done[(gc - 1) & 1], ((gc - 1) >> 1) & 1)) break;
         tc_fence_after();
       }
       if (live && half == 0) {
@@ -460,8 +452,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
       for (int o = half * (D / 2); o < (half + 1) * (D / 2); o += 32) {
         float y[32] = {};
 #pragma unroll 1
-        for (int i = 0; i < min(nt, 2); ++i) {
-          const int g = g0 ^ i;
+        for (int g = 0; g < (nt > 0 ? 2 : 0); ++g) {
           uint32_t x[32];
           tmem_ld_32x32b_x32(lane_tmem + G::OCOL + g * D + o, x);
           tmem_ld_wait();
