@@ -2,22 +2,29 @@
 // per request and K/V head (prompt chunks): a tile of 128 rows against tiles of 128
 // keys, S = Q K^T and O += P V on tcgen05 with the cached codes as they are.
 //
-// A row is a lane; two threads share it, one for each half of a tile's keys, and
-// agree on its reference.
+// A row is a lane; the two groups of softmax warps take the halves of a tile's keys,
+// each with references, sums and outputs of its own, and meet at the end of a piece.
 //   S = Q K^T   K's codes as they are (kind::f8f6f4), the query row as the sum of two
 //               E4M3 values times its power of two, 2^-e (q1 + q2): exact for what
 //               bf16 holds down to 2^-9 of the row's largest element, within 2^-17
-//   O += P V    f16: four warps widen each V tile once for all 128 rows (exact, times
-//               its block's power of two); weights have 11 bits.  Splitting weights
-//               into three 8-bit terms instead took 4.75 instructions per weight next
-//               to 0.5, and half as long again on the tensor cores: 934 us for three
-//               chunks of 1.5-2.1K tokens after 0.5-4K.
-// A tile is 512 + 512 cycles of products at D = 128, next to 512 of exponentials (a
-// quarter per cycle and scheduler); S and V's f16 form are double buffered so that
-// all run at a time.
+//   O += P V    f16: V's codes widened once per tile for all 128 rows (exact), the
+//               power of two of a value's block times the weight in P, which has 11
+//               bits and takes the place of S in TMEM.  Splitting weights into three
+//               8-bit terms instead took 4.75 instructions per weight next to 0.5, and
+//               half as long again on the tensor cores.
+// A tile is 512 + 512 cycles of products at D = 128 and 512 of exponentials (a quarter
+// per cycle and scheduler), at once in principle.  Measured, three chunks of 1.5-2.1K
+// tokens after 0.5-4K, 8 heads to one of the cache: 339 us, 675 TFLOP/s, 34% of what
+// the products alone would need; DRAM is idle.  What bounds it is the length of the
+// chain softmax, P V, next S of a buffer (about 4900 cycles for two tiles; half of the
+// products or a quarter of the exponentials each take off only 10%), and of its parts
+// the softmax's instruction issue: 1270 slots per tile and scheduler.  Straight-line
+// code in place of the small loops is slower in each place that was tried (339 -> 347
+// with the weights' loop unrolled): warps of five roles share a scheduler's
+// instruction fetch.
 //
 // Ring, division of the work and join as in kv_attention.cu; one CTA per SM.  Warps
-// 0-7 softmax, 8 copies, 9 products, 12-15 widen V.
+// 0-7 softmax, 8 copies, 9 products, 10-11 query rows of the next piece, 12-15 widen V.
 #include "kv_attention.cuh"
 
 namespace nvfp4moe {
@@ -350,18 +357,23 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
           return fminf(fmaxf(qs * heads.kscale[hd][k >> p.shift], 1.175494351e-38f), 3.402823466e38f);
         };
         float top = -INFINITY;
-#pragma unroll 1
-        for (int k = 64 * half; k < 64 * half + 64; k += 16) {
-          uint32_t x[16];
-          tmem_ld16(s_tmem + k, x);
-          const float c0 = factor(k);
-          tmem_ld_wait();
-          float mx[4];
+        {
+          uint32_t x[2][32];
+          tmem_ld_32x32b_x32(s_tmem + 64 * half, x[0]);
+          tmem_ld_32x32b_x32(s_tmem + 64 * half + 32, x[1]);
+          float c[4];
 #pragma unroll
-          for (int j = 0; j < 4; ++j)
-            mx[j] = fmaxf(fmaxf(__uint_as_float(x[4 * j]), __uint_as_float(x[4 * j + 1])),
-                          fmaxf(__uint_as_float(x[4 * j + 2]), __uint_as_float(x[4 * j + 3])));
-          top = fmaxf(top, fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * c0);
+          for (int h = 0; h < 4; ++h) c[h] = factor(64 * half + 16 * h);
+          tmem_ld_wait();
+#pragma unroll
+          for (int h = 0; h < 4; ++h) {
+            float mx = -INFINITY;
+#pragma unroll
+            for (int j = 0; j < 16; j += 2)
+              mx = fmaxf(fmaxf(mx, __uint_as_float(x[h >> 1][(h & 1) * 16 + j])),
+                         __uint_as_float(x[h >> 1][(h & 1) * 16 + j + 1]));
+            top = fmaxf(top, mx * c[h]);
+          }
         }
         const int unit1 = max(unit, vr.y);
         if (__any_sync(0xFFFFFFFFu, top > ref + kRowSlack || (m == -INFINITY && top != -INFINITY)) || unit1 != unit) {
