@@ -48,39 +48,50 @@ __device__ __forceinline__ float block_sum(float v, float* part) {
   return v;
 }
 
-// One CTA per row, the row in registers: NI vectors of eight elements per thread.
+// One CTA per row, the row in registers: NI vectors of eight elements per thread, all
+// loads from memory issued before the first sum.
 template <typename A, int NI>
-__global__ void __launch_bounds__(1024) block_norm_kernel(const NormParams p) {
+__global__ void __launch_bounds__(1024 / (NI > 2 ? 2 : 1)) block_norm_kernel(const NormParams p) {
   __shared__ float part[2][32];
   pdl_wait();
   pdl_trigger();
   const int64_t t = blockIdx.x;
   const int nv = p.H / 8;
-  float y[NI][8];
-  const bool has_a = p.a != nullptr;
-  float sum = 0.0f;
+  const bool has_a = p.a != nullptr, gate_c = p.gate != nullptr && p.gate_ld_c != 0;
+  constexpr int AW = sizeof(A) == 4 ? 2 : 1;
+  uint4 wa[NI][AW], wx[NI], wg[NI];
 #pragma unroll
   for (int k = 0; k < NI; ++k) {
     const int i = k * blockDim.x + threadIdx.x;
 #pragma unroll
-    for (int c = 0; c < 8; ++c) y[k][c] = 0.0f;
-    if (i < nv && has_a) {
-      if constexpr (sizeof(A) == 4) {
-        const float4* s = reinterpret_cast<const float4*>(static_cast<const float*>(p.a) + t * p.ld_a) + 2 * i;
-        const float4 u = s[0], v = s[1];
-        y[k][0] = u.x, y[k][1] = u.y, y[k][2] = u.z, y[k][3] = u.w;
-        y[k][4] = v.x, y[k][5] = v.y, y[k][6] = v.z, y[k][7] = v.w;
-      } else {
-        unpack8(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.a) + t * p.ld_a)[i], y[k]);
-      }
+    for (int j = 0; j < AW; ++j) wa[k][j] = make_uint4(0, 0, 0, 0);
+    wx[k] = wg[k] = make_uint4(0, 0, 0, 0);
+    if (i >= nv) continue;
+    if (has_a) {
 #pragma unroll
-      for (int c = 0; c < 8; ++c) sum += y[k][c] * y[k][c];
+      for (int j = 0; j < AW; ++j)
+        wa[k][j] = reinterpret_cast<const uint4*>(static_cast<const A*>(p.a) + t * p.ld_a)[i * AW + j];
     }
+    wx[k] = reinterpret_cast<const uint4*>(p.x + t * p.ld_x)[i];
+    if (gate_c) wg[k] = reinterpret_cast<const uint4*>(p.gate + t * p.gate_ld_t)[i];
+  }
+  const float g1 = p.gate != nullptr && !gate_c ? __bfloat162float(p.gate[t * p.gate_ld_t]) : 1.0f;
+  float y[NI][8], sum = 0.0f;
+#pragma unroll
+  for (int k = 0; k < NI; ++k) {
+    if constexpr (AW == 2) {
+      const uint4 u = wa[k][0], v = wa[k][1];
+      const uint32_t w[8] = {u.x, u.y, u.z, u.w, v.x, v.y, v.z, v.w};
+#pragma unroll
+      for (int c = 0; c < 8; ++c) y[k][c] = __uint_as_float(w[c]);
+    } else {
+      unpack8(wa[k][0], y[k]);
+    }
+#pragma unroll
+    for (int c = 0; c < 8; ++c) sum += y[k][c] * y[k][c];
   }
   float r = p.alpha;
   if (has_a && p.w_post != nullptr) r *= rsqrtf(block_sum(sum, part[0]) / (float)p.H + p.eps);
-  float g1 = 1.0f;
-  if (p.gate != nullptr && p.gate_ld_c == 0) g1 = __bfloat162float(p.gate[t * p.gate_ld_t]);
   sum = 0.0f;
 #pragma unroll
   for (int k = 0; k < NI; ++k) {
@@ -95,18 +106,16 @@ __global__ void __launch_bounds__(1024) block_norm_kernel(const NormParams p) {
 #pragma unroll
         for (int c = 0; c < 8; ++c) y[k][c] *= v[c];
       }
-      if (p.gate != nullptr) {
-        if (p.gate_ld_c) {
-          unpack8(reinterpret_cast<const uint4*>(p.gate + t * p.gate_ld_t)[i], v);
+      if (gate_c) {
+        unpack8(wg[k], v);
 #pragma unroll
-          for (int c = 0; c < 8; ++c) y[k][c] *= v[c];
-        } else {
+        for (int c = 0; c < 8; ++c) y[k][c] *= v[c];
+      } else {
 #pragma unroll
-          for (int c = 0; c < 8; ++c) y[k][c] *= g1;
-        }
+        for (int c = 0; c < 8; ++c) y[k][c] *= g1;
       }
     }
-    unpack8(reinterpret_cast<const uint4*>(p.x + t * p.ld_x)[i], v);
+    unpack8(wx[k], v);
 #pragma unroll
     for (int c = 0; c < 8; ++c) {
       y[k][c] += v[c];
@@ -128,11 +137,22 @@ __global__ void __launch_bounds__(1024) block_norm_kernel(const NormParams p) {
   }
 }
 
+template <typename A, int NI>
+cudaError_t launch(const NormParams& p, cudaStream_t st) {
+  return launch_pdl(block_norm_kernel<A, NI>, p.T, (p.H / 8 + 32 * NI - 1) / (32 * NI) * 32, 0, st, p);
+}
+
+// Few rows: a row over as many threads as possible, for the shortest chain.  From two
+// rows per SM on, several vectors per thread, so that more rows are at work on an SM
+// and more loads in flight.  8192 rows, one / two / three / four vectors: H = 2048
+// 25.9 / 23.9 / 25.5 / 27.7 us, 4096 53 / 47 / 47 / 49, 6144 94 / 68 / 62 / 76, 8192
+// 134 / 98 / 102 / 106; 12288 at two, three and four 200 / 126 / 204.
 template <typename A>
 cudaError_t launch(const NormParams& p, cudaStream_t st) {
   const int nv = p.H / 8;
-  if (nv <= 1024) return launch_pdl(block_norm_kernel<A, 1>, p.T, (nv + 31) / 32 * 32, 0, st, p);
-  return launch_pdl(block_norm_kernel<A, 2>, p.T, ((nv + 1) / 2 + 31) / 32 * 32, 0, st, p);
+  if (p.T < 2 * num_sms() || nv <= 128) return nv <= 1024 ? launch<A, 1>(p, st) : launch<A, 2>(p, st);
+  if (nv <= 512) return launch<A, 2>(p, st);
+  return nv <= 1536 ? launch<A, 3>(p, st) : launch<A, 4>(p, st);
 }
 
 }  // namespace
