@@ -161,13 +161,13 @@ __global__ void __launch_bounds__(kPlanThreads) kv_plan_kernel(const PlanParams 
 //
 // A CTA per chunk of tokens, head and half of the cache: it finds the runs of
 // consecutive slots in a page that start there, and of each run the largest magnitude,
-// the block's exponent, then the codes.  A run of up to kShortRun rows is one warp's,
-// a longer one the whole CTA's, with its rows in registers in between.
+// the block's exponent, then the codes, with the rows in registers in between.  A run
+// of up to four accesses is one warp's, a longer one the whole CTA's.
 // ---------------------------------------------------------------------------
 
-constexpr int kAppendThreads = 256;  // 512 for pages of 128 rows of 128
-constexpr int kShortRun = 8;
-constexpr int kRunWords = 5;         // 32 tokens each: a chunk and 127 rows after its last token
+constexpr int kAppendThreads = 256;  // 512 for pages of 128 rows of 128: four rows of a page per thread
+constexpr int kChunk = 64;
+constexpr int kRunWords = 6;         // 32 tokens each: a chunk and the 127 rows after its last token
 
 struct AppendParams {
   const void *k, *v;
@@ -176,7 +176,7 @@ struct AppendParams {
   uint8_t *k_codes, *k_exps, *v_codes, *v_exps;
   int32_t* dev_status;
   int64_t num_slots;
-  int T, Hkv, shift, chunk_shift;
+  int T, Hkv, shift, chunk;
 };
 
 template <typename X>
@@ -206,158 +206,110 @@ __device__ __forceinline__ int block_exponent(float amax) {
   return e < -127 ? -127 : e;  // zeros and subnormals too
 }
 
-// Where a run goes.
 template <typename X, int D>
-struct Run {
-  const X* x;
-  int64_t ld;
-  uint8_t *codes, *exps;
-  int o, e0;  // its first row in the page; the block's exponent if it holds rows before
-  __device__ __forceinline__ Run(const AppendParams& p, int t, int32_t slot, int head, int half) {
-    const int S = 1 << p.shift;
-    ld = half ? p.ld_v : p.ld_k;
-    x = static_cast<const X*>(half ? p.v : p.k) + (int64_t)t * ld + head * D;
-    const int64_t block = (int64_t)(slot >> p.shift) * p.Hkv + head;
-    codes = (half ? p.v_codes : p.k_codes) + block * S * D;
-    exps = (half ? p.v_exps : p.k_exps) + block;
-    o = slot & (S - 1);
-    e0 = o > 0 ? (int)*exps - 127 : -127;
-  }
-  // the block's exponent after the run; rescales the rows before it (rows r0, r0 + step, ...)
-  __device__ __forceinline__ int settle(float amax, int r0, int step, int c0) const {
-    const int e = block_exponent(amax);
-    if (e <= e0 || o == 0) return max(e, e0);
-    const float f = exp2_int(e0 - e < -127 ? -127 : e0 - e);
-#pragma unroll 4
-    for (int r = r0; r < o; r += step) {
-      uint2* w = reinterpret_cast<uint2*>(codes + r * D + c0);
-      const uint2 was = *w;
-      *w = make_uint2(kv::rescale_codes(was.x, f), kv::rescale_codes(was.y, f));
-    }
-    return e;
-  }
-  __device__ __forceinline__ void put(int r, int c0, const float (&v)[8], float f) const {
-    *reinterpret_cast<uint2*>(codes + (o + r) * D + c0) =
-        make_uint2(kv::encode4(v[0] * f, v[1] * f, v[2] * f, v[3] * f),
-                   kv::encode4(v[4] * f, v[5] * f, v[6] * f, v[7] * f));
-  }
-};
-
-template <typename X, int D>
-__global__ void __launch_bounds__(512) kv_append_kernel(const AppendParams p) {
+__global__ void __launch_bounds__(512, 2) kv_append_kernel(const AppendParams p) {
   constexpr int LPR = D / 8;  // lanes of a row, eight elements each
+  constexpr int M = 4, W = sizeof(X) / 2;
   __shared__ float tops[16];
-  __shared__ int32_t slot_of[32];
-  __shared__ uint32_t starts_s, goes_on[kRunWords + 1];
+  __shared__ int32_t slots[32 * kRunWords];
+  __shared__ uint32_t goes_on[kRunWords + 1];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, warps = blockDim.x >> 5;
-  const int half = blockIdx.x & 1, head = (int)(blockIdx.x >> 1) % p.Hkv;
-  const int first = (int)((blockIdx.x >> 1) / p.Hkv) << p.chunk_shift;
+  const int half = blockIdx.x & 1, head = (int)(blockIdx.x >> 1) % p.Hkv, S = 1 << p.shift;
+  const int first = (int)((blockIdx.x >> 1) / p.Hkv) * p.chunk;
   const int c0 = (lane % LPR) * 8;
   pdl_wait();
   pdl_trigger();
-  // the tokens that start a run and those that go on with one, a word per warp
+  // the tokens that go on with the run before them, a word per warp
   if (warp <= kRunWords) {
-    const int tl = first + warp * 32 + lane;
+    const int tl = first + tid;
     const bool there = warp < kRunWords && tl < p.T;
     const int32_t slot = there ? p.slots[tl] : -1, before = there && tl > 0 ? p.slots[tl - 1] : -1;
-    const bool goes = slot >= 0 && (slot & ((1 << p.shift) - 1)) != 0 && before == slot - 1;
-    const uint32_t on = __ballot_sync(0xFFFFFFFFu, goes);
+    const uint32_t on = __ballot_sync(0xFFFFFFFFu, slot >= 0 && (slot & (S - 1)) != 0 && before == slot - 1);
     if (lane == 0) goes_on[warp] = on;
-    if (warp == 0) {
-      const bool begins = slot >= 0 && !goes && lane < 1 << p.chunk_shift, bad = begins && slot >= p.num_slots;
-      if (bad) report_status(p.dev_status, NVFP4_E_BAD_PAGE);
-      const uint32_t starts = __ballot_sync(0xFFFFFFFFu, begins && !bad);
-      if (lane == 0) starts_s = starts;
-      slot_of[lane] = slot;
-    }
+    if (warp < kRunWords) slots[tid] = slot;
   }
   __syncthreads();
-  const uint32_t starts = starts_s;
-  auto length = [&](int i) {
-    int at = i + 1;
-    for (;;) {
-      const int c = __ffs(~(goes_on[at >> 5] >> (at & 31))) - 1;  // (ones end with the word at the latest)
-      if (c >= 0) at += min(c, 32 - (at & 31));
-      else at += 32;
-      if ((at & 31) != 0 || !(goes_on[at >> 5] & 1)) return at - i;
-    }
-  };
-
   int turn = 0;
-  for (uint32_t todo = starts; todo; todo &= todo - 1) {
-    const int i = __ffs(todo) - 1;
-    const int32_t slot = slot_of[i];
-    if (turn++ % warps != warp) continue;
-    const int n = length(i);
-    if (n > kShortRun) continue;
-    constexpr int RPW = 32 / LPR, M = kShortRun / RPW;
-    const Run<X, D> run(p, first + i, slot, head, half);
-    const int r0 = lane / LPR;
-    float v[M][8], amax = 0.0f;
+  for (int t0 = 0; t0 < p.chunk; t0 += 32) {
+    // a lane per token: the run that starts there
+    const int32_t mine = slots[t0 + lane];
+    const bool begins = t0 + lane < p.chunk && mine >= 0 && !(goes_on[t0 >> 5] >> lane & 1);
+    const bool bad = begins && mine >= p.num_slots;
+    if (bad) report_status(p.dev_status, NVFP4_E_BAD_PAGE);
+    int rows = 0;
+    if (begins && !bad) {
+      int at = t0 + lane + 1;
+      for (;;) {
+        const uint32_t w = ~(goes_on[at >> 5] >> (at & 31));  // (ones end with the word at the latest)
+        at += w ? min(__ffs(w) - 1, 32 - (at & 31)) : 32;
+        if ((at & 31) != 0 || !(goes_on[at >> 5] & 1)) break;
+      }
+      rows = at - t0 - lane;
+    }
+    constexpr int kShort = M * (32 / LPR);
+#pragma unroll 1
+    for (int together = 0; together < 2; ++together) {  // the warps' runs, then the CTA's
+      uint32_t todo = __ballot_sync(0xFFFFFFFFu, together ? rows > kShort : rows > 0 && rows <= kShort);
+#pragma unroll 1
+      for (; todo; todo &= todo - 1) {
+        if (!together && turn++ % warps != warp) continue;
+        const int i = __ffs(todo) - 1, n = __shfl_sync(0xFFFFFFFFu, rows, i);
+        const int32_t slot = slots[t0 + i];
+        const int o = slot & (S - 1);  // its first row in the page
+        const int64_t ld = half ? p.ld_v : p.ld_k;
+        const int64_t block = (int64_t)(slot >> p.shift) * p.Hkv + head;
+        uint8_t* exps = (half ? p.v_exps : p.k_exps) + block;
+        const int e0 = o > 0 ? (int)*exps - 127 : -127;  // the block's exponent if it holds rows before
+        const int step = (together ? blockDim.x : 32) / LPR, r0 = (together ? tid : lane) / LPR;
+        const X* x = static_cast<const X*>(half ? p.v : p.k) + (first + t0 + i + r0) * ld + head * D + c0;
+        uint4 w[M][W];
 #pragma unroll
-    for (int k = 0; k < M; ++k) {
-      if (r0 + k * RPW < n) {
-        load8<X>(run.x + (r0 + k * RPW) * run.ld + c0, v[k]);
-      } else {
+        for (int k = 0; k < M; ++k)
 #pragma unroll
-        for (int j = 0; j < 8; ++j) v[k][j] = 0.0f;
+          for (int j = 0; j < W; ++j)
+            w[k][j] = r0 + k * step < n ? reinterpret_cast<const uint4*>(x + k * step * ld)[j] : make_uint4(0, 0, 0, 0);
+        float amax = 0.0f;
+#pragma unroll
+        for (int k = 0; k < M; ++k) {
+          float v[8];
+          load8<X>(reinterpret_cast<const X*>(w[k]), v);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) amax = fmaxf(amax, fabsf(v[j]));
+        }
+#pragma unroll
+        for (int d = 16; d > 0; d >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, d));
+        if (together) {
+          if (lane == 0) tops[warp] = amax;
+          __syncthreads();
+          for (int k = 0; k < warps; ++k) amax = fmaxf(amax, tops[k]);
+        }
+        uint8_t* codes = (half ? p.v_codes : p.k_codes) + block * S * D + c0;
+        int e = block_exponent(amax);
+        if (e > e0 && o > 0) {  // the rows before in the block's new scale
+          const float f = exp2_int(e0 - e < -127 ? -127 : e0 - e);
+#pragma unroll 1
+          for (int r = r0; r < o; r += step) {
+            uint2* c = reinterpret_cast<uint2*>(codes + r * D);
+            const uint2 was = *c;
+            *c = make_uint2(kv::rescale_codes(was.x, f), kv::rescale_codes(was.y, f));
+          }
+        }
+        e = max(e, e0);
+        const float f = exp2_int(-e);
+#pragma unroll
+        for (int k = 0; k < M; ++k) {
+          float v[8];
+          load8<X>(reinterpret_cast<const X*>(w[k]), v);
+          if (r0 + k * step < n)
+            *reinterpret_cast<uint2*>(codes + (o + r0 + k * step) * D) =
+                make_uint2(kv::encode4(v[0] * f, v[1] * f, v[2] * f, v[3] * f),
+                           kv::encode4(v[4] * f, v[5] * f, v[6] * f, v[7] * f));
+        }
+        if (together) __syncthreads();  // tops and the old exponent are read
+        else __syncwarp();
+        if ((together ? tid : lane) == 0) *exps = (uint8_t)(e + 127);
       }
     }
-#pragma unroll
-    for (int k = 0; k < M; ++k)
-#pragma unroll
-      for (int j = 0; j < 8; ++j) amax = fmaxf(amax, fabsf(v[k][j]));
-#pragma unroll
-    for (int d = 16; d > 0; d >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, d));
-    const int e = run.settle(amax, r0, RPW, c0);
-    const float f = exp2_int(-e);
-#pragma unroll
-    for (int k = 0; k < M; ++k)
-      if (r0 + k * RPW < n) run.put(r0 + k * RPW, c0, v[k], f);
-    __syncwarp();  // every lane has read the old exponent
-    if (lane == 0) *run.exps = (uint8_t)(e + 127);
-  }
-
-  for (uint32_t todo = starts; todo; todo &= todo - 1) {
-    const int i = __ffs(todo) - 1;
-    const int32_t slot = slot_of[i];
-    const int n = length(i);
-    if (n <= kShortRun) continue;
-    constexpr int M = 4, W = sizeof(X) / 2;
-    const int RPC = blockDim.x / LPR;  // (at least a quarter of a page)
-    const Run<X, D> run(p, first + i, slot, head, half);
-    const int r0 = tid / LPR;
-    uint4 w[M][W];
-#pragma unroll
-    for (int k = 0; k < M; ++k)
-#pragma unroll
-      for (int j = 0; j < W; ++j)
-        w[k][j] = r0 + k * RPC < n ? reinterpret_cast<const uint4*>(run.x + (r0 + k * RPC) * run.ld + c0)[j]
-                                   : make_uint4(0, 0, 0, 0);
-    float amax = 0.0f;
-#pragma unroll
-    for (int k = 0; k < M; ++k) {
-      float v[8];
-      load8<X>(reinterpret_cast<const X*>(w[k]), v);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) amax = fmaxf(amax, fabsf(v[j]));
-    }
-#pragma unroll
-    for (int d = 16; d > 0; d >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, d));
-    if (lane == 0) tops[warp] = amax;
-    __syncthreads();  // (every thread has read the old exponent)
-#pragma unroll
-    for (int k = 0; k < 16; ++k) amax = fmaxf(amax, k < warps ? tops[k] : 0.0f);
-    const int e = run.settle(amax, r0, RPC, c0);
-    const float f = exp2_int(-e);
-#pragma unroll
-    for (int k = 0; k < M; ++k) {
-      float v[8];
-      load8<X>(reinterpret_cast<const X*>(w[k]), v);
-      if (r0 + k * RPC < n) run.put(r0 + k * RPC, c0, v, f);
-    }
-    if (tid == 0) *run.exps = (uint8_t)(e + 127);
-    __syncthreads();  // (tops is read)
   }
 }
 
@@ -384,11 +336,10 @@ cudaError_t launch_kv_append(const void* k, const void* v, int x_dtype, int64_t 
                              int32_t* dev_status, cudaStream_t st) {
   AppendParams p = {k, v, ld_k, ld_v, slots, k_codes, k_exps, v_codes, v_exps, dev_status, num_pages * page_size,
                     T, Hkv, kv::log2_page(page_size), 0};
-  // 32 tokens per CTA where that fills the GPU, else 8, one per warp
-  p.chunk_shift = ((int64_t)T >> 5) * Hkv * 2 >= num_sms() ? 5 : 3;
-  const int64_t chunks = ((int64_t)T + (1 << p.chunk_shift) - 1) >> p.chunk_shift;
-  const unsigned grid = (unsigned)(chunks * Hkv * 2);
-  const int threads = page_size * D > 8192 ? 512 : kAppendThreads;  // four rows of a page per thread
+  // kChunk tokens per CTA where that fills the GPU, else 8, one per warp
+  p.chunk = (int64_t)T * Hkv * 2 >= (int64_t)num_sms() * kChunk ? kChunk : 8;
+  const unsigned grid = (unsigned)(((int64_t)T + p.chunk - 1) / p.chunk * Hkv * 2);
+  const int threads = page_size * D > 8192 ? 512 : kAppendThreads;
   if (x_dtype == NVFP4_DT_BF16)
     return D == 128 ? launch_pdl(kv_append_kernel<__nv_bfloat16, 128>, grid, threads, 0, st, p)
                     : launch_pdl(kv_append_kernel<__nv_bfloat16, 64>, grid, threads, 0, st, p);
