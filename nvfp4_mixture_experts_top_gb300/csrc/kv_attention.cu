@@ -255,7 +255,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
       const int seen0 = it.rq.kv - it.rq.n;                             // keys before the first query's own
       const int all_see = it.rq.n == 1 ? kv_len : seen0 + row0 / group + 1;  // keys below this are seen by every row
       const int key_first = it.t0 * kTile;
-      if (first && tid == 0) p.cut[blockIdx.x] = {it.u0, span, out_row, hk, nrows, {0, 0, 0}};
+      if (first && tid == 0) p.cut[blockIdx.x] = cut_of(it, it.lo, it.all, it.ctas, group);
       for (int r = tid; r < R; r += 128) {
         const int rr = out_row + r, tok = rr / group;
         row_at[r] = tok * p.Hq + hk * group + rr - tok * group;
@@ -510,7 +510,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
       softmax_barrier();  // the rows' values are read
       first = false;
     }
-    if (first && tid == 0) p.cut[blockIdx.x].before = 0;
+    if (first && tid == 0) p.cut[blockIdx.x].parts = 0;
   }
   tc_fence_before();
   __syncthreads();

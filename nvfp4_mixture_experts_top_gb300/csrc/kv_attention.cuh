@@ -20,16 +20,11 @@ constexpr int kPieceCost = 3;    // what a sequence costs besides its tiles, in 
 constexpr int kNoPage = -1000;   // value exponent of keys that have no page
 constexpr int kFarExp = -60;     // value blocks further below the largest one count as this far
 
-// The sequence that a CTA's range starts in, for the join: its work before the
-// range and in all, its first output row (token * group + head in group), K/V
-// head and rows.
+// A sequence that was cut, for the join, at the second CTA that has a part of it: the
+// number of parts (0: the CTA is no such), where the first one is, and the first output
+// row (token * group + head in group), K/V head and rows.
 struct Cut {
-  int32_t before, span, row, head, rows, pad[3];
-};
-// The work of the whole call, and the CTAs that share it (0: nothing is cut).
-struct Total {
-  int64_t work;
-  int32_t ctas;
+  int32_t parts, first, row, head, rows, pad[3];
 };
 
 struct Params {
@@ -39,7 +34,6 @@ struct Params {
   __nv_bfloat16* out;
   float* lse;
   int32_t* dev_status;
-  Total* total;
   Cut* cut;         // [CTA]
   float* part;      // [CTA][2][rows][D] outputs of a CTA's first and last sequence
   float* part_lse;  // [CTA][2][rows] their log2-sums
@@ -155,6 +149,8 @@ template <int R>
 struct Pieces : Piece {
   int64_t off;   // work of the request before the position
   int64_t left;  // work of the range after the position
+  int64_t lo, all;  // where the range starts, and the work in all (0: nothing is cut)
+  int ctas;         // that have a range
 
   __device__ __forceinline__ bool next(const Params& p, int group) {
     if (left <= 0) return false;
@@ -223,16 +219,14 @@ __device__ __forceinline__ void range_of_cta(const Params& p, int group, Pieces<
 #pragma unroll
   for (int w = 0; w < W; ++w) longest = max(longest, x.longest[w]);
   const bool split = longest > kWholeKeys;
-  int64_t total = 0, all = 0, before = split ? in_w - work : in_s - seqs;
+  int64_t total = 0, before = split ? in_w - work : in_s - seqs;
 #pragma unroll
   for (int w = 0; w < W; ++w) {
     const int64_t n = x.sum[split ? 1 : 0][w];
     total += n;
-    all += x.sum[1][w];
     if (w < warp) before += n;
   }
   const int ctas = (int)min(total, (int64_t)gridDim.x), c = blockIdx.x;
-  if (c == 0 && tid == 0) *p.total = {all, split ? ctas : 0};
   if (c < ctas) {
     const Shares sh(total, ctas);
     const int64_t lo = sh.start(c), n = sh.start(c + 1) - lo;
@@ -252,6 +246,9 @@ __device__ __forceinline__ void range_of_cta(const Params& p, int group, Pieces<
     it.b = x.b;
     it.off = x.off;
     it.left = n;
+    it.lo = lo;
+    it.all = split ? total : 0;
+    it.ctas = ctas;
     if (!split) {  // sequences to work
       int64_t rest = n, skip = it.off;
       it.left = 0;
@@ -278,6 +275,21 @@ __device__ __noinline__ static bool wait_on(uint64_t* bar, uint32_t parity, vola
 __device__ __forceinline__ bool lean_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag,
                                           int32_t* dev_status) {
   return __all_sync(0xFFFFFFFFu, mbar_try_wait(bar, parity)) || wait_on(bar, parity, abort_flag, dev_status);
+}
+
+// What the join is told of the first piece of a CTA's range (first: of its parts).
+__device__ __forceinline__ Cut cut_of(const Piece& x, int64_t lo, int64_t all, int ctas, int group) {
+  Cut cut = {0, 0, x.rq.q0 * group + x.row0, x.hk, x.nrows, {0, 0, 0}};
+  const int c = blockIdx.x;
+  if (all > 0 && x.u0 > 0) {
+    const Shares sh(all, ctas);
+    const int64_t a = lo - x.u0;  // where the sequence starts
+    if (sh.start(c - 1) <= a) {
+      cut.parts = sh.owner(a + x.span - 1) - c + 2;
+      cut.first = (c - 1) * 2 + (sh.start(c - 1) == a ? 0 : 1);
+    }
+  }
+  return cut;
 }
 
 // What the copying warp says of a tile: scale and exponent of its pages, and the
@@ -367,66 +379,69 @@ __device__ __forceinline__ void copy_tiles(const Params& p, int group, It& it, c
   }
 }
 
-// Joins the partial results of a sequence that was cut by CTAs: CTA c - 1 takes
-// the one that the range of CTA c of the attention starts in, if no range before
-// c starts inside it.  A warp per row, parts in order.
+// Joins the partial results of the sequences that were cut: block x per Cut, a row per
+// kJoinWarps warps, each a share of the parts in order, with loads of four parts in
+// flight.  A part per CTA: part 0 of the sequence that its range starts in, the first
+// one perhaps part 1.  Few instructions, for they are fetched anew in each call: with
+// the statistics first, over lanes, and a warp or eight rows to a CTA it took 39 us of
+// three 2K chunks' 343 and 13 of 60 us at one request of 131K keys.
+template <int R>
+constexpr int kJoinWarps = R == 128 ? 1 : 4;
+
 template <int D, int R>
 __global__ void __launch_bounds__(256) kv_attention_join_kernel(const Params p) {
-  constexpr int E = D / 32;
+  constexpr int E = D / 32, Q = kJoinWarps<R>;
+  __shared__ float stat[8][2], sums[8][D];
   pdl_wait();
   pdl_trigger();
-  const int c = blockIdx.x + 1, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const Total all = *p.total;
+  const int c = blockIdx.x + 1, lane = threadIdx.x & 31, warp = threadIdx.x >> 5, q = warp % Q;
   const Cut cut = p.cut[c];
-  if (c >= all.ctas || cut.before == 0) return;
-  const Shares sh(all.work, all.ctas);
-  const int64_t a = sh.start(c) - cut.before;
-  const int c0 = sh.owner(a);
-  if (sh.owner(a + cut.before - 1) != c0) return;
-  // a part per CTA: part 0 of the sequence that its range starts in, else part 1
-  const int n = sh.owner(a + cut.span - 1) - c0 + 1;
-  const int first = c0 * 2 + (sh.start(c0) >= a ? 0 : 1);
-  for (int r = warp; r < cut.rows; r += 8) {
-    float top = -INFINITY, sum = 0.0f, acc[E] = {};
-    for (int k0 = 0; k0 < n; k0 += 32) {
-      const int m = min(32, n - k0), k = k0 + min(lane, m - 1);
-      const int row = (k == 0 ? first : (c0 + k) * 2) * R + r;
-      const float z = lane < m ? p.part_lse[row] : -INFINITY;
-      float mx = z;
+  const int n = cut.parts, r = blockIdx.y * (8 / Q) + warp / Q;
+  if (n == 0 || blockIdx.y * (8 / Q) >= cut.rows) return;
+  float top = -INFINITY, sum = 0.0f, acc[E] = {};
+  auto add = [&](float z, float s, const float (&y)[E]) {
+    const float t = fmaxf(top, z), ref = t == -INFINITY ? 0.0f : t, f = ex2(top - ref), w = ex2(z - ref);
+    top = t;
+    sum = sum * f + s * w;
 #pragma unroll
-      for (int d = 16; d > 0; d >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, d));
-      const float t1 = fmaxf(top, mx), ms = t1 == -INFINITY ? 0.0f : t1, f = ex2(top - ms), w = ex2(z - ms);
-      top = t1;
-      sum = sum * f + w;
-#pragma unroll
-      for (int i = 0; i < E; ++i) acc[i] *= f;
-#pragma unroll 16
-      for (int i = 0; i < m; ++i) {
-        const float wi = __shfl_sync(0xFFFFFFFFu, w, i);
-        const float* src = p.part + (int64_t)__shfl_sync(0xFFFFFFFFu, row, i) * D + lane * E;
-        if constexpr (E == 4) {
-          const float4 y = *reinterpret_cast<const float4*>(src);
-          acc[0] += wi * y.x, acc[1] += wi * y.y, acc[2] += wi * y.z, acc[3] += wi * y.w;
-        } else {
-          const float2 y = *reinterpret_cast<const float2*>(src);
-          acc[0] += wi * y.x, acc[1] += wi * y.y;
-        }
-      }
+    for (int i = 0; i < E; ++i) acc[i] = acc[i] * f + w * y[i];
+  };
+  if (r < cut.rows) {
+#pragma unroll 4
+    for (int k = n * q / Q; k < n * (q + 1) / Q; ++k) {
+      const int64_t row = (int64_t)(k == 0 ? cut.first : (c - 1 + k) * 2) * R + r;
+      const float* src = p.part + row * D + lane * E;
+      float y[E];
+      if constexpr (E == 4) *reinterpret_cast<float4*>(y) = *reinterpret_cast<const float4*>(src);
+      else *reinterpret_cast<float2*>(y) = *reinterpret_cast<const float2*>(src);
+      add(p.part_lse[row], 1.0f, y);
     }
-#pragma unroll
-    for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, d);
-    const bool empty = sum == 0.0f;
-    const float inv = empty ? 0.0f : reciprocal(sum);
-    const int group = p.Hq / p.Hkv, rr = cut.row + r;
-    const int64_t at = (int64_t)(rr / group) * p.Hq + cut.head * group + rr % group;
-#pragma unroll
-    for (int i = 0; i < E; i += 2) {
-      const __nv_bfloat162 x =
-          __floats2bfloat162_rn(empty ? 0.0f : acc[i] * inv, empty ? 0.0f : acc[i + 1] * inv);
-      *reinterpret_cast<__nv_bfloat162*>(p.out + at * D + lane * E + i) = x;
-    }
-    if (p.lse != nullptr && lane == 0) p.lse[at] = empty ? -INFINITY : (top + lg2(sum)) * 0.6931471805599453f;
   }
+  if constexpr (Q > 1) {
+    if (lane == 0) stat[warp][0] = top, stat[warp][1] = sum;
+#pragma unroll
+    for (int i = 0; i < E; ++i) sums[warp][lane * E + i] = acc[i];
+    __syncthreads();
+    if (q > 0) return;
+#pragma unroll 1
+    for (int k = 1; k < Q; ++k) {
+      float y[E];
+#pragma unroll
+      for (int i = 0; i < E; ++i) y[i] = sums[warp + k][lane * E + i];
+      add(stat[warp + k][0], stat[warp + k][1], y);
+    }
+  }
+  if (r >= cut.rows) return;
+  const bool empty = sum == 0.0f;
+  const float inv = empty ? 0.0f : reciprocal(sum);
+  const int group = p.Hq / p.Hkv, rr = cut.row + r;
+  const int64_t at = (int64_t)(rr / group) * p.Hq + cut.head * group + rr % group;
+#pragma unroll
+  for (int i = 0; i < E; i += 2) {
+    const __nv_bfloat162 x = __floats2bfloat162_rn(empty ? 0.0f : acc[i] * inv, empty ? 0.0f : acc[i + 1] * inv);
+    *reinterpret_cast<__nv_bfloat162*>(p.out + at * D + lane * E + i) = x;
+  }
+  if (p.lse != nullptr && lane == 0) p.lse[at] = empty ? -INFINITY : (top + lg2(sum)) * 0.6931471805599453f;
 }
 
 // Lays out the workspace of `ctas` CTAs.
@@ -439,12 +454,10 @@ size_t carve(Params* p, void* base, size_t ctas) {
     off += (bytes + 255) & ~(size_t)255;
     return at;
   };
-  uint8_t* total = take(sizeof(Total));
   uint8_t* cut = take(ctas * sizeof(Cut));
   uint8_t* lse = take(ctas * 2 * R * sizeof(float));
   uint8_t* part = take(ctas * 2 * R * D * sizeof(float));
   if (p != nullptr) {
-    p->total = reinterpret_cast<Total*>(total);
     p->cut = reinterpret_cast<Cut*>(cut);
     p->part_lse = reinterpret_cast<float*>(lse);
     p->part = reinterpret_cast<float*>(part);
@@ -456,7 +469,7 @@ size_t carve(Params* p, void* base, size_t ctas) {
 template <int D, int R, typename K>
 cudaError_t launch(K kernel, int per_sm, int threads, int smem_bytes, const KvAttention& a, cudaStream_t st) {
   Params p = {static_cast<const __nv_bfloat16*>(a.q), a.k_exps, a.v_exps, a.table, a.kv_lens, a.query_start,
-              static_cast<__nv_bfloat16*>(a.out), a.lse, a.dev_status, nullptr, nullptr, nullptr, nullptr, a.ld_q,
+              static_cast<__nv_bfloat16*>(a.out), a.lse, a.dev_status, nullptr, nullptr, nullptr, a.ld_q,
               a.ld_table, a.num_pages, a.M, a.T, a.B, a.Hq, a.Hkv, log2_page(a.page_size), a.scale};
   const int ctas = num_sms() * per_sm;
   carve<D, R>(&p, a.workspace, ctas);
@@ -470,7 +483,7 @@ cudaError_t launch(K kernel, int per_sm, int threads, int smem_bytes, const KvAt
   e = launch_pdl(kernel, ctas, threads, smem_bytes, st, tm_k, tm_v, p);
   // a table that holds no sequence long enough to be cut needs no join
   if (e != cudaSuccess || (int64_t)a.M * a.page_size <= kWholeKeys) return e;
-  return launch_pdl(kv_attention_join_kernel<D, R>, ctas - 1, 256, 0, st, p);
+  return launch_pdl(kv_attention_join_kernel<D, R>, dim3(ctas - 1, R * kJoinWarps<R> / 8), 256, 0, st, p);
 }
 
 }  // namespace kv

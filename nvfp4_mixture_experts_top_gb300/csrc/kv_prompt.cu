@@ -115,8 +115,8 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
   pdl_wait();
   pdl_trigger();  // after this CTA's TMEM allocation
   const uint32_t tmem = tmem_s;
-  Pieces<kRows> it;  // (the query rows' warps go by it, the others by what these pass on)
-  range_of_cta<kPromptThreads, kRows>(p, group, it, scratch);
+  Pieces<kRows> range;  // (the query rows' warps go by it, the others by what these pass on)
+  range_of_cta<kPromptThreads, kRows>(p, group, range, scratch);
   Feed feed;
   feed.at = pieces;
   feed.full = q_full;
@@ -235,15 +235,15 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
     constexpr int LPR = D / 16;
     const int t = tid - 10 * 32, c = t % LPR;
     for (int qn = 0;; ++qn) {
-      const bool more = it.next(p, group);
+      const bool more = range.next(p, group);
       const int qb = qn & 1;
       if (!wait(&q_empty[qb], ((qn >> 1) & 1) ^ 1)) break;
       if (t == 0) {
-        pieces[qb] = it;
+        pieces[qb] = range;
         if (!more) pieces[qb].nt = -1;
       }
       uint8_t* q8 = smem + G::QOFF + qb * (2 * kRows * D);
-      const int rows = more && it.nt > 0 ? kRows : 0;
+      const int rows = more && range.nt > 0 ? kRows : 0;
       constexpr int UR = 4;  // loads in flight
 #pragma unroll 1
       for (int r0 = t / LPR; r0 < rows; r0 += UR * (64 / LPR)) {
@@ -252,10 +252,10 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
         for (int u = 0; u < UR; ++u) {
           const int r = r0 + u * (64 / LPR);
           w[u][0] = w[u][1] = make_uint4(0, 0, 0, 0);
-          if (r < it.nrows) {
-            const int qr = it.row0 + r, qt = qr / group;
-            const uint4* src = reinterpret_cast<const uint4*>(p.q + (int64_t)(it.rq.q0 + qt) * p.ld_q +
-                                                              (int64_t)(it.hk * group + qr - qt * group) * D + 16 * c);
+          if (r < range.nrows) {
+            const int qr = range.row0 + r, qt = qr / group;
+            const uint4* src = reinterpret_cast<const uint4*>(p.q + (int64_t)(range.rq.q0 + qt) * p.ld_q +
+                                                              (int64_t)(range.hk * group + qr - qt * group) * D + 16 * c);
             w[u][0] = src[0];
             w[u][1] = src[1];
           }
@@ -317,8 +317,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
       if (nt < 0) break;
       const bool live = row < it.nrows;
       const int64_t at = (int64_t)(it.rq.q0 + tok) * p.Hq + it.hk * group + rr - tok * group;
-      if (first && tid == 0)
-        p.cut[blockIdx.x] = {it.u0, it.span, it.rq.q0 * group + it.row0, it.hk, it.nrows, {0, 0, 0}};
+      if (first && tid == 0) p.cut[blockIdx.x] = cut_of(it, range.lo, range.all, range.ctas, group);
       // keys that the row sees; that all of the tile's rows see
       const int lim = live ? min(it.rq.kv, it.rq.kv - it.rq.n + tok + 1) : 0;
       const int all_see = it.rq.kv - it.rq.n + it.row0 / group + 1;
@@ -493,7 +492,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
       tc_fence_before();
       if (!both()) break;  // (both groups' outputs are read)
     }
-    if (first && tid == 0) p.cut[blockIdx.x].before = 0;
+    if (first && tid == 0) p.cut[blockIdx.x].parts = 0;
   }
   tc_fence_before();
   __syncthreads();
