@@ -3,23 +3,27 @@
 //
 // Both products run on tcgen05 with the cached codes as they are: keys are the
 // 128-row side of S^T = K Q^T, the head dimension that of O^T = V^T P^T, and the
-// query rows -- R of 8, 16, 32 or 64 of one request and K/V head -- the column
-// side.  What meets the codes is split into E4M3 terms, each in columns of its
-// own (kind::f8f6f4 takes E4M3 at twice the rate of f16):
-//   q = 2^-e (q1 + q2 / 16)        exact for what bf16 holds down to 2^-9 of the
-//                                  row's largest element, within 2^-18 of it
-//   p = p1 + p2 / 16 (+ p3 / 256)  8 significant bits (12 with the third term,
-//                                  up to R = 16 where the columns are free)
+// query rows -- R of 8 or 16 of one request and K/V head -- the column side.  What
+// meets the codes is split into 8-bit terms, each in columns of its own
+// (kind::f8f6f4 takes them at twice the rate of f16):
+//   q = 2^-e (q1 + q2 / 16)       E4M3: exact for what bf16 holds down to 2^-9 of the
+//                                 row's largest element, within 2^-18 of it
+//   p = p1 + p2 / 8 + p3 / 64     E5M2: 9 significant bits over a range of 2^-16
 // fp32 accumulation of E4M3 products was measured exact to 2^-21 of the largest
-// term.  No K or V element passes through registers: an earlier form that widened
+// term.  No K or V element passes through registers: a form that widened
 // them to f16 for mma.sync needed 620 instructions per 32 keys and stayed at 69%
 // of the HBM rate, bound by their issue.
 //
-// Few rows: every cached byte is read once for all query heads of a K/V head, and
-// 2 * D bytes per key and 4 * D * R flops leave HBM as the limit; copies run ahead
-// of the arithmetic across the ends of sequences.  Many rows (prompts): the
-// softmax between the products bounds it (32 exponentials per SM and cycle, and
-// about 10 instructions per weight on four warps).
+// Every cached byte is read once for all query heads of a K/V head; 2 * D bytes per
+// key and 4 * D * R flops leave HBM as the limit, and copies run ahead of the
+// arithmetic across the ends of sequences.  512 requests of 0.1-4K keys, D = 128:
+// 176.5 us for 1.07 GB, 6.0 TB/s, 90% of the rate of a plain copy.  Shorter calls are
+// bound by their ends: one request of 131K keys, 268 MB, 51 us, of which the first
+// product comes after 5 us and the join takes 5; 16 of 8K, 150 MB, 32 us.
+//
+// More than 16 rows go to the kernel for prompts (kv_prompt.cu): 256 requests of 8
+// tokens with 4 heads each, 1-3K keys, D = 128, take 160 us there and took 188 in a
+// form of this kernel for 32 rows; 16 rows take 103 us here and 158 there.
 //
 // A CTA: warps 0-3 softmax (a key per thread), warp 4 page look-ups and TMA copies
 // of tiles of 128 keys, warp 5 MMA issue.  Two CTAs per SM, so that one's softmax
@@ -86,9 +90,9 @@ struct Geo {
   static constexpr int NP = (TERMS * R + 15) / 16 * 16;       // columns of O (and of P)
   static constexpr int SBUFS = 2;
   static constexpr int OCOL = SBUFS * NS;
-  static constexpr int COLS = OCOL + NP <= 64 ? 64 : (OCOL + NP <= 128 ? 128 : 256);
+  static constexpr int COLS = OCOL + NP <= 64 ? 64 : 128;
   static constexpr int SUB_BYTES = kTile * D;                 // K or V of a tile
-  static constexpr int SUBS = D == 64 ? 8 : (R <= 16 ? 6 : 5);
+  static constexpr int SUBS = D == 64 ? 8 : 6;
   static constexpr int POFF = 0, QOFF = kTile * NP, ROFF = QOFF + NS * D;  // P, Q, ring
   static constexpr int SMEM_BYTES = ROFF + SUBS * SUB_BYTES;
   static_assert(ROFF % 1024 == 0 && QOFF % 1024 == 0, "swizzle atoms");
@@ -530,7 +534,6 @@ cudaError_t launch_rows(const KvAttention& a, cudaStream_t st) {
   const int64_t rows = (int64_t)a.max_query_len * (a.Hq / a.Hkv);
   return rows <= 8    ? launch_few<D, 8>(a, st)
          : rows <= 16 ? launch_few<D, 16>(a, st)
-         : rows <= 32 ? launch_few<D, 32>(a, st)
                       : launch_kv_prompt(a, st);
 }
 
@@ -539,7 +542,7 @@ cudaError_t launch_rows(const KvAttention& a, cudaStream_t st) {
 size_t kv_attention_ws_bytes(int T, int B, int Hq, int Hkv, int D) {
   (void)T, (void)B, (void)Hq, (void)Hkv;
   const size_t ctas = (size_t)num_sms() * kCtasPerSm;
-  const size_t few = D == 128 ? carve<128, 32>(nullptr, nullptr, ctas) : carve<64, 32>(nullptr, nullptr, ctas);
+  const size_t few = D == 128 ? carve<128, 16>(nullptr, nullptr, ctas) : carve<64, 16>(nullptr, nullptr, ctas);
   return few > kv_prompt_ws_bytes(D) ? few : kv_prompt_ws_bytes(D);
 }
 

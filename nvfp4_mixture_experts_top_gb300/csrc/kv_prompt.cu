@@ -14,12 +14,12 @@
 //               half as long again on the tensor cores.
 // A tile is 512 + 512 cycles of products at D = 128 and 512 of exponentials (a quarter
 // per cycle and scheduler), at once in principle.  Measured, three chunks of 1.5-2.1K
-// tokens after 0.5-4K, 8 heads to one of the cache: 339 us, 675 TFLOP/s, 34% of what
-// the products alone would need; DRAM is idle.  What bounds it is the length of the
+// tokens after 0.5-4K, 8 heads to one of the cache: 311 us, 735 TFLOP/s, 37% of the
+// rate of a plain bf16 product; DRAM is idle.  What bounds it is the length of the
 // chain softmax, P V, next S of a buffer (about 4900 cycles for two tiles; half of the
 // products or a quarter of the exponentials each take off only 10%), and of its parts
 // the softmax's instruction issue: 1270 slots per tile and scheduler.  Straight-line
-// code in place of the small loops is slower in each place that was tried (339 -> 347
+// code in place of the small loops is slower in each place that was tried (339 -> 347 us
 // with the weights' loop unrolled): warps of five roles share a scheduler's
 // instruction fetch.
 //
