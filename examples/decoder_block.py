@@ -1,0 +1,131 @@
+"""A decoder block over the paged 8-bit cache: prompts, then single tokens.
+
+    python examples/decoder_block.py [--requests 8] [--prompt 300] [--steps 16]
+
+One block of a decoder as a serving loop runs it, on synthetic weights:
+
+    h = norm(x)                                                   block_norm
+    q, k, v = h W_qkv                                             (a library product)
+    pages, slots and lengths of the new tokens                    kv_plan
+    k, v into the cache                                           kv_append
+    a = attention of q over the cache                             kv_attention
+    x = x + norm(a W_o), h = norm(x)                              block_norm
+    m = experts(h), routed by h W_r                               moe_router_logits, moe_layer_forward
+    x = x + norm(m), h = norm(x) for the next block               block_norm
+
+Lengths, tables and the list of free pages stay on the GPU: a step needs nothing
+from the one before it on the host.  Positions are not encoded.
+"""
+import argparse
+import os
+import sys
+
+import torch
+
+sys.path.insert(0, os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
+from nvfp4_mixture_experts_top_gb300 import binding as B  # noqa: E402
+
+BF = torch.bfloat16
+
+
+class Cache:
+    """The paged cache of one block: codes, exponents, tables, free pages, lengths."""
+
+    def __init__(self, requests, pages, tokens_max, Hkv, D, page_size, device):
+        self.page_size = page_size
+        shape = (pages, Hkv, page_size, D)
+        self.k, self.v = (torch.empty(shape, dtype=torch.uint8, device=device) for _ in range(2))
+        self.ke, self.ve = (torch.empty(shape[:2], dtype=torch.uint8, device=device) for _ in range(2))
+        self.table = torch.full((requests, -(-tokens_max // page_size)), -1, dtype=torch.int32, device=device)
+        self.free = torch.arange(pages, dtype=torch.int32, device=device)
+        self.free_count = torch.full((1,), pages, dtype=torch.int32, device=device)
+        self.lens = torch.zeros(requests, dtype=torch.int32, device=device)
+
+    def arrays(self):
+        return self.k, self.ke, self.v, self.ve
+
+
+class Block:
+    """Weights of one block and the work of one step through it."""
+
+    def __init__(self, H=1024, Hq=16, Hkv=4, D=64, E=16, I=512, top_k=4, seed=0, device="cuda"):
+        g = torch.Generator(device=device).manual_seed(seed)
+
+        def rand(*s, by):
+            return torch.randn(*s, generator=g, device=device) * by
+
+        self.H, self.Hq, self.Hkv, self.D, self.top_k = H, Hq, Hkv, D, top_k
+        self.w_qkv = rand(H, (Hq + 2 * Hkv) * D, by=H ** -0.5).to(BF)
+        self.w_o = rand(Hq * D, H, by=(Hq * D) ** -0.5).to(BF)
+        self.w_router = rand(E, H, by=H ** -0.5).to(BF)
+        self.norms = [(1 + rand(H, by=0.1)).to(BF) for _ in range(4)]
+        self.w13 = self._experts(rand(E, 2 * I, H, by=H ** -0.5))
+        self.w2 = self._experts(rand(E, H, I, by=I ** -0.5))
+        self.S_h = torch.tensor([2.0 ** -8], device=device)
+        self.status = torch.zeros(1, dtype=torch.int32, device=device)
+
+    @staticmethod
+    def _experts(w):
+        E, N, K = w.shape
+        codes, scales, S = zip(*(B.nvfp4_quantize(e) for e in w))
+        return torch.stack(codes), B.nvfp4_pack_weight_scales(torch.stack(scales), E, N, K), torch.cat(S)
+
+    def enter(self, x):
+        """The first block's norm of its input."""
+        return B.block_norm(x, w_pre=self.norms[0])[1]
+
+    def step(self, x, h, new, max_new, cache, w_next):
+        """x, h [T, H]: the residual stream (updated in place) and its norm, the new
+        tokens of all requests in order; new int32 [requests] their counts, at most
+        max_new each.  Returns x, the norm for the next block and what was in between."""
+        T, D, Hq, Hkv = x.shape[0], self.D, self.Hq, self.Hkv
+        qkv = h @ self.w_qkv
+        q, k, v = (t.unflatten(1, (-1, D)) for t in qkv.split([Hq * D, Hkv * D, Hkv * D], 1))
+        plan = B.kv_plan(cache.lens, new, cache.table, cache.free, cache.free_count, cache.page_size, T, self.status)
+        B.kv_append(k, v, plan["slot_map"], cache.k, cache.ke, cache.v, cache.ve, self.status)
+        a = B.kv_attention(q, *cache.arrays(), cache.table, plan["kv_lens"], plan["query_start"], max_new,
+                           dev_status=self.status)
+        x, h1 = B.block_norm(x, a.flatten(1) @ self.w_o, w_post=self.norms[1], w_pre=self.norms[2], y=x)
+        logits = B.moe_router_logits(h1, self.w_router, dev_status=self.status)
+        m = B.moe_layer_forward(B.MOE_W4A4, h1, logits, self.top_k, self.w13, self.w2, self.S_h, dev_status=self.status)
+        x, h2 = B.block_norm(x, m, w_post=self.norms[3], w_pre=w_next, y=x)
+        cache.lens, cache.free_count = plan["kv_lens"], plan["free_left"]
+        return x, h2, dict(plan, q=q, k=k, v=v, a=a, h1=h1, m=m)
+
+
+def main():
+    ap = argparse.ArgumentParser(description=__doc__.splitlines()[0])
+    ap.add_argument("--requests", type=int, default=8)
+    ap.add_argument("--prompt", type=int, default=300, help="longest prompt, in tokens")
+    ap.add_argument("--steps", type=int, default=16, help="single tokens after the prompt")
+    args = ap.parse_args()
+    dev, n = "cuda", args.requests
+    block = Block(device=dev)
+    S, most = 64, args.prompt + args.steps
+    lens = [max(1, args.prompt - 37 * b) for b in range(n)]
+    new = torch.tensor(lens, dtype=torch.int32, device=dev)
+    one = torch.ones(n, dtype=torch.int32, device=dev)
+    g = torch.Generator(device=dev).manual_seed(1)
+    for _ in range(2):  # (the first time loads the kernels)
+        cache = Cache(n, n * -(-most // S), most, block.Hkv, block.D, S, dev)
+        events = [torch.cuda.Event(enable_timing=True) for _ in range(3)]
+        x = torch.randn(sum(lens), block.H, generator=g, device=dev).to(BF)
+        events[0].record()
+        x, h, seen = block.step(x, block.enter(x), new, max(lens), cache, block.norms[0])
+        ends = seen["query_start"][1:].long() - 1
+        x, h = x[ends], h[ends]
+        events[1].record()
+        for _ in range(args.steps):  # each request's last row goes on as its next token
+            x, h, seen = block.step(x, h, one, 1, cache, block.norms[0])
+        events[2].record()
+        torch.cuda.synchronize()
+    if int(block.status):
+        raise SystemExit("status %d" % int(block.status))
+    print("prompts: %d tokens in %.3f ms" % (sum(lens), events[0].elapsed_time(events[1])))
+    print("tokens: %d steps of %d requests, %.3f ms a step" % (args.steps, n,
+                                                               events[1].elapsed_time(events[2]) / max(args.steps, 1)))
+    print("lengths %s, %d of %d pages free" % (cache.lens.tolist(), int(cache.free_count), cache.free.numel()))
+
+
+if __name__ == "__main__":
+    main()

@@ -50,6 +50,13 @@ def test_sizes_and_types(T, H, a):
     _check(*_case(T, H, a, "none", a is not None, True, T + H, dev))
 
 
+@pytest.mark.parametrize("H", [264, 1032, 4096, 4104, 6152, 12288, 12296, 16384])
+@pytest.mark.parametrize("a,gate", [(None, "none"), (BF, "channel"), (torch.float32, "full"), (BF, "token")])
+def test_many_rows(H, a, gate):
+    dev = cuda_or_skip()
+    _check(*_case(333, H, a, gate, a is not None, True, H, dev), alpha=0.7)
+
+
 @pytest.mark.parametrize("gate", ["none", "channel", "token", "full"])
 @pytest.mark.parametrize("post,pre", [(True, True), (True, False), (False, True), (False, False)])
 @pytest.mark.parametrize("T", [1, 37])

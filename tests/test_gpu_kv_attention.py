@@ -104,6 +104,15 @@ def test_prompts(ctx, new, Hq, Hkv, D, S):
     _check(_case(ctx, new, Hq, Hkv, D, S, 11, dev))
 
 
+@pytest.mark.parametrize("ctx,new,Hq,Hkv,D,S", [
+    ([0], [1500], 7, 1, 128, 64), ([0, 600, 0], [900, 30, 1], 6, 2, 64, 16), ([100], [333], 71, 1, 64, 32),
+    ([0, 0, 0], [300, 301, 302], 24, 2, 128, 16), ([1, 2500, 9], [700, 2, 17], 20, 4, 128, 128),
+])
+def test_prompts_cut_between_row_tiles_of_growing_length(ctx, new, Hq, Hkv, D, S):
+    dev = cuda_or_skip()
+    _check(_case(ctx, new, Hq, Hkv, D, S, 13, dev))
+
+
 def test_prompts_next_to_single_tokens_and_absent_requests():
     dev = cuda_or_skip()
     ctx, new = [700, 0, 33, 5000, 0, 12, 64], [1, 300, 0, 1, 1, 40, 1]

@@ -136,6 +136,26 @@ def test_append_matches_the_restatement(dtype, lens, new, Hkv, D, S):
     assert int(st.item()) == 0
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("lens,new,Hkv,D,S", [
+    ([0, 77, 3], [900, 1, 1200], 8, 128, 128), ([65, 0, 1], [700, 700, 70], 8, 64, 128),
+    ([9, 0], [1000, 333], 8, 64, 16), ([0] * 9 + [40], [1] * 9 + [1500], 8, 128, 64), ([50], [2500], 4, 64, 32),
+    ([200 + i for i in range(1300)], [1] * 1300, 4, 64, 16)])
+def test_append_many_tokens(dtype, lens, new, Hkv, D, S):
+    """Chunks of many tokens per CTA: runs that pass a chunk's end, whole pages, next to single tokens."""
+    dev = cuda_or_skip()
+    k, v, slots, P = _append_case(lens, new, Hkv, D, S, dtype, S + D, dev)
+    halves = [ref.make_cache(P, Hkv, S, D, 3 + i, dev, spread=4) for i in (0, 1)]
+    want = [(c.clone(), e.clone()) for c, e in halves]
+    for x, (c, e) in zip((k, v), want):
+        ref.append(x.double(), slots, c, e)
+    st = torch.zeros(1, dtype=torch.int32, device=dev)
+    B.kv_append(k, v, _i32(slots, dev), *halves[0], *halves[1], dev_status=st)
+    for g, w in zip(halves, want):
+        _same_cache(g, w)
+    assert int(st.item()) == 0
+
+
 def test_append_special_values():
     """Zeros, subnormals, infinities, NaN, the largest finite value, and 448 * 2^e exactly."""
     dev = cuda_or_skip()
