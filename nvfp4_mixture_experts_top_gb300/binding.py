@@ -597,8 +597,9 @@ def _refuse(what):
 
 def _cache_dims(k_codes, k_exps, v_codes, v_exps):
     shape = k_codes.shape
-    if len(shape) != 4 or not (_is(k_codes, _U8, shape) and _is(v_codes, _U8, shape) and _is(k_exps, _U8, shape[:2]) and
-                               _is(v_exps, _U8, shape[:2])):
+    if (len(shape) != 4 or v_codes.shape != shape or k_exps.shape != shape[:2] or v_exps.shape != shape[:2] or
+            not (k_codes.dtype is v_codes.dtype is k_exps.dtype is v_exps.dtype is _U8 and k_codes.is_contiguous() and
+                 v_codes.is_contiguous() and k_exps.is_contiguous() and v_exps.is_contiguous())):
         _refuse("the cache must be contiguous uint8: codes [P, Hkv, S, D] and exps [P, Hkv], keys and values alike")
     return shape
 
