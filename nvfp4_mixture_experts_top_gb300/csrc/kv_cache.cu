@@ -214,12 +214,13 @@ __global__ void __launch_bounds__(512, 2) kv_append_kernel(const AppendParams p)
   __shared__ int32_t slots[32 * kRunWords];
   __shared__ uint32_t goes_on[kRunWords + 1];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, warps = blockDim.x >> 5;
-  const int half = blockIdx.x & 1, head = (int)(blockIdx.x >> 1) % p.Hkv, S = 1 << p.shift;
-  const int first = (int)((blockIdx.x >> 1) / p.Hkv) * p.chunk;
+  const int head = (int)blockIdx.x % p.Hkv, S = 1 << p.shift;
+  const int first = (int)(blockIdx.x / p.Hkv) * p.chunk;
   const int c0 = (lane % LPR) * 8;
   pdl_wait();
   pdl_trigger();
   // the tokens that go on with the run before them, a word per warp
+  if (tid < 16) tops[tid] = 0.0f;
   if (warp <= kRunWords) {
     const int tl = first + tid;
     const bool there = warp < kRunWords && tl < p.T;
@@ -256,58 +257,73 @@ __global__ void __launch_bounds__(512, 2) kv_append_kernel(const AppendParams p)
         const int i = __ffs(todo) - 1, n = __shfl_sync(0xFFFFFFFFu, rows, i);
         const int32_t slot = slots[t0 + i];
         const int o = slot & (S - 1);  // its first row in the page
-        const int64_t ld = half ? p.ld_v : p.ld_k;
-        const int64_t block = (int64_t)(slot >> p.shift) * p.Hkv + head;
-        uint8_t* exps = (half ? p.v_exps : p.k_exps) + block;
-        const int e0 = o > 0 ? (int)*exps - 127 : -127;  // the block's exponent if it holds rows before
-        const int step = (together ? blockDim.x : 32) / LPR, r0 = (together ? tid : lane) / LPR;
-        const X* x = static_cast<const X*>(half ? p.v : p.k) + (first + t0 + i + r0) * ld + head * D + c0;
-        uint4 w[M][W];
-#pragma unroll
-        for (int k = 0; k < M; ++k)
-#pragma unroll
-          for (int j = 0; j < W; ++j)
-            w[k][j] = r0 + k * step < n ? reinterpret_cast<const uint4*>(x + k * step * ld)[j] : make_uint4(0, 0, 0, 0);
-        float amax = 0.0f;
-#pragma unroll
-        for (int k = 0; k < M; ++k) {
-          float v[8];
-          load8<X>(reinterpret_cast<const X*>(w[k]), v);
-#pragma unroll
-          for (int j = 0; j < 8; ++j) amax = fmaxf(amax, fabsf(v[j]));
-        }
-#pragma unroll
-        for (int d = 16; d > 0; d >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, d));
-        if (together) {
-          if (lane == 0) tops[warp] = amax;
-          __syncthreads();
-          for (int k = 0; k < warps; ++k) amax = fmaxf(amax, tops[k]);
-        }
-        uint8_t* codes = (half ? p.v_codes : p.k_codes) + block * S * D + c0;
-        int e = block_exponent(amax);
-        if (e > e0 && o > 0) {  // the rows before in the block's new scale
-          const float f = exp2_int(e0 - e < -127 ? -127 : e0 - e);
 #pragma unroll 1
-          for (int r = r0; r < o; r += step) {
-            uint2* c = reinterpret_cast<uint2*>(codes + r * D);
-            const uint2 was = *c;
-            *c = make_uint2(kv::rescale_codes(was.x, f), kv::rescale_codes(was.y, f));
-          }
-        }
-        e = max(e, e0);
-        const float f = exp2_int(-e);
+        for (int half = blockIdx.y; half < 2; half += gridDim.y) {  // keys, values
+          const int64_t ld = half ? p.ld_v : p.ld_k;
+          const int64_t block = (int64_t)(slot >> p.shift) * p.Hkv + head;
+          uint8_t* exps = (half ? p.v_exps : p.k_exps) + block;
+          const int e0 = o > 0 ? (int)*exps - 127 : -127;  // the block's exponent if it holds rows before
+          const int step = (together ? blockDim.x : 32) / LPR, r0 = (together ? tid : lane) / LPR;
+          const X* x = static_cast<const X*>(half ? p.v : p.k) + (first + t0 + i + r0) * ld + head * D + c0;
+          uint4 w[M][W];
 #pragma unroll
-        for (int k = 0; k < M; ++k) {
-          float v[8];
-          load8<X>(reinterpret_cast<const X*>(w[k]), v);
-          if (r0 + k * step < n)
-            *reinterpret_cast<uint2*>(codes + (o + r0 + k * step) * D) =
-                make_uint2(kv::encode4(v[0] * f, v[1] * f, v[2] * f, v[3] * f),
-                           kv::encode4(v[4] * f, v[5] * f, v[6] * f, v[7] * f));
+          for (int k = 0; k < M; ++k)
+#pragma unroll
+            for (int j = 0; j < W; ++j)
+              w[k][j] = r0 + k * step < n ? reinterpret_cast<const uint4*>(x + k * step * ld)[j] : make_uint4(0, 0, 0, 0);
+          float amax = 0.0f;  // (of two numbers, should one be NaN, both forms of the maximum take the other)
+          if constexpr (W == 1) {
+            __nv_bfloat162 top = __float2bfloat162_rn(0.0f);
+#pragma unroll
+            for (int k = 0; k < M; ++k) {
+              const __nv_bfloat162* v = reinterpret_cast<const __nv_bfloat162*>(w[k]);
+#pragma unroll
+              for (int j = 0; j < 4; ++j) top = __hmax2(top, __habs2(v[j]));
+            }
+            amax = fmaxf(__low2float(top), __high2float(top));
+          } else {
+#pragma unroll
+            for (int k = 0; k < M; ++k) {
+              const float* v = reinterpret_cast<const float*>(w[k]);
+#pragma unroll
+              for (int j = 0; j < 8; ++j) amax = fmaxf(amax, fabsf(v[j]));
+            }
+          }
+#pragma unroll
+          for (int d = 16; d > 0; d >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, d));
+          if (together) {
+            if (lane == 0) tops[warp] = amax;
+            __syncthreads();
+            amax = tops[lane & 15];
+#pragma unroll
+            for (int d = 8; d > 0; d >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, d));
+          }
+          uint8_t* codes = (half ? p.v_codes : p.k_codes) + block * S * D + c0;
+          int e = block_exponent(amax);
+          if (e > e0 && o > 0) {  // the rows before in the block's new scale
+            const float f = exp2_int(e0 - e < -127 ? -127 : e0 - e);
+#pragma unroll 1
+            for (int r = r0; r < o; r += step) {
+              uint2* c = reinterpret_cast<uint2*>(codes + r * D);
+              const uint2 was = *c;
+              *c = make_uint2(kv::rescale_codes(was.x, f), kv::rescale_codes(was.y, f));
+            }
+          }
+          e = max(e, e0);
+          const float f = exp2_int(-e);
+#pragma unroll
+          for (int k = 0; k < M; ++k) {
+            float v[8];
+            load8<X>(reinterpret_cast<const X*>(w[k]), v);
+            if (r0 + k * step < n)
+              *reinterpret_cast<uint2*>(codes + (o + r0 + k * step) * D) =
+                  make_uint2(kv::encode4(v[0] * f, v[1] * f, v[2] * f, v[3] * f),
+                             kv::encode4(v[4] * f, v[5] * f, v[6] * f, v[7] * f));
+          }
+          if (together) __syncthreads();  // tops and the old exponent are read
+          else __syncwarp();
+          if ((together ? tid : lane) == 0) *exps = (uint8_t)(e + 127);
         }
-        if (together) __syncthreads();  // tops and the old exponent are read
-        else __syncwarp();
-        if ((together ? tid : lane) == 0) *exps = (uint8_t)(e + 127);
       }
     }
   }
@@ -338,7 +354,8 @@ cudaError_t launch_kv_append(const void* k, const void* v, int x_dtype, int64_t 
                     T, Hkv, kv::log2_page(page_size), 0};
   // kChunk tokens per CTA where that fills the GPU, else 8, one per warp
   p.chunk = (int64_t)T * Hkv * 2 >= (int64_t)num_sms() * kChunk ? kChunk : 8;
-  const unsigned grid = (unsigned)(((int64_t)T + p.chunk - 1) / p.chunk * Hkv * 2);
+  // keys and values by the same CTA where there are many
+  const dim3 grid((unsigned)(((int64_t)T + p.chunk - 1) / p.chunk * Hkv), p.chunk == kChunk ? 1 : 2);
   const int threads = page_size * D > 8192 ? 512 : kAppendThreads;
   if (x_dtype == NVFP4_DT_BF16)
     return D == 128 ? launch_pdl(kv_append_kernel<__nv_bfloat16, 128>, grid, threads, 0, st, p)
