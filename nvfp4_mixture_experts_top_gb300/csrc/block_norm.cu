@@ -2,6 +2,12 @@
 // addition in one pass:
 //   u = a * rsqrt(mean(a^2) + eps) * w_post
 //   y = x + alpha * gate * u,   h = y * rsqrt(mean(y^2) + eps) * w_pre
+//
+// Two sums over a row in turn, so a row is one CTA's and stays in its registers in
+// fp32; y and h are rounded to bf16 once each, h from the unrounded y.  HBM bounds it:
+// 8191 rows of 6144 (bf16, per-channel gate, both weights; 403 MB) take 62.5 us, 6.4
+// TB/s, 96% of the rate of a plain copy.  16 rows of 4096 take 2.6 us, a launch and two
+// memory latencies.
 #include "common.cuh"
 #include "kernels.h"
 

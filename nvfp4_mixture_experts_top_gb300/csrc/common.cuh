@@ -193,15 +193,6 @@ __host__ __device__ constexpr uint32_t idesc_bf16(uint32_t M, uint32_t N) {
          | ((M >> 4) << 24);
 }
 
-// Instruction descriptor, kind::f8f6f4 with E4M3 inputs and fp32 accumulate;
-// both operands K-major, or both MN-major (transposed).
-__host__ __device__ constexpr uint32_t idesc_e4m3(uint32_t M, uint32_t N, bool mn_major) {
-  return (1u << 4)                            // D format: F32
-         | (mn_major ? (3u << 15) : 0u)       // A and B are MN-major
-         | ((N >> 3) << 17)
-         | ((M >> 4) << 24);
-}
-
 // Warp-collective TMEM load: 32 lanes x 32 consecutive 32-bit columns.
 __device__ __forceinline__ void tmem_ld_32x32b_x32(uint32_t taddr, uint32_t (&r)[32]) {
   asm volatile(

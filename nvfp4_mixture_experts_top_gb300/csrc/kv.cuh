@@ -76,6 +76,15 @@ __device__ __forceinline__ uint32_t swizzled(int r, int c) {
   return D == 128 ? r * 128 + ((c ^ (r & 7)) << 4) : r * 64 + ((c ^ (r >> 1 & 3)) << 4);
 }
 
+// Instruction descriptor, kind::f8f6f4 with E4M3 inputs and fp32 accumulate;
+// both operands K-major, or both MN-major (transposed).
+__host__ __device__ constexpr uint32_t idesc_e4m3(uint32_t M, uint32_t N, bool mn_major) {
+  return (1u << 4)                            // D format: F32
+         | (mn_major ? (3u << 15) : 0u)       // A and B are MN-major
+         | ((N >> 3) << 17)
+         | ((M >> 4) << 24);
+}
+
 // D[tmem] (+)= A[smem] * B[smem], E4M3 operands, fp32 accumulation (M = 128, K = 32).
 __device__ __forceinline__ void ew_mma_e4m3(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
                                             uint32_t accumulate) {

@@ -18,8 +18,8 @@
 // key and 4 * D * R flops leave HBM as the limit, and copies run ahead of the
 // arithmetic across the ends of sequences.  512 requests of 0.1-4K keys, D = 128:
 // 176.5 us for 1.07 GB, 6.0 TB/s, 90% of the rate of a plain copy.  Shorter calls are
-// bound by their ends: one request of 131K keys, 268 MB, 51 us, of which the first
-// product comes after 5 us and the join takes 5; 16 of 8K, 150 MB, 32 us.
+// bound by their ends: one request of 333 keys takes 7.6 us; one of 131K, 268 MB, 51,
+// 5 of them the join's; 16 of 8K, 150 MB, 32, with SMs busy 85% of the time.
 //
 // More than 16 rows go to the kernel for prompts (kv_prompt.cu): 256 requests of 8
 // tokens with 4 heads each, 1-3K keys, D = 128, take 160 us there and took 188 in a

@@ -14,7 +14,8 @@ namespace {
 // -- then every new page and every new token on its own.  A few kilobytes of
 // integers: the time is one launch plus a short chain of dependent loads, so
 // every CTA repeats the prefix sums (8 bytes of lengths per request, from L2)
-// rather than waiting for another one to do it.
+// rather than waiting for another one to do it.  16 requests: 2.6 us; 509 requests
+// with prompts among them: 4.0 us.
 // ---------------------------------------------------------------------------
 
 constexpr int kPlanThreads = 512;
@@ -163,6 +164,15 @@ __global__ void __launch_bounds__(kPlanThreads) kv_plan_kernel(const PlanParams 
 // consecutive slots in a page that start there, and of each run the largest magnitude,
 // the block's exponent, then the codes, with the rows in registers in between.  A run
 // of up to four accesses is one warp's, a longer one the whole CTA's.
+//
+// The maximum has to be known before the first code, so a run is read whole; from
+// registers it is read once.  The codes' rounding is E4M3's own, after an exact
+// product with a power of two.  Seven prompts of 0.9-1.3K tokens, 8 heads of 128
+// (47 MB): 13.8 us, 3.4 TB/s, half the rate of a copy; 16 single tokens: 3.3 us.  What
+// bounds the prompts is a CTA's chain -- slots, rows, maximum, codes, three round
+// trips for one page -- at four CTAs per SM: encoding nothing takes off 0.9 us, chunks
+// of 32 tokens add 2.8.  A warp per run without the search per chunk took 39.5 us, a
+// warp per 32 tokens 26.4 (2.6 for the single tokens).
 // ---------------------------------------------------------------------------
 
 constexpr int kAppendThreads = 256;  // 512 for pages of 128 rows of 128: four rows of a page per thread
