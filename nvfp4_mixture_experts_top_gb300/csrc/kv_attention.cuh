@@ -16,7 +16,8 @@ namespace kv {
 constexpr int kTile = 128;       // keys of a step
 constexpr int kWholeKeys = 512;  // if no sequence is longer, none is cut
 constexpr int kHeads = 8;        // tile headers in flight
-constexpr int kPieceCost = 3;    // what a sequence costs besides its tiles, in tiles
+constexpr int kPieceCost = 3;    // what a sequence costs besides its tiles, in tiles (2 / 3 / 5: 512 requests of
+                                 // 0.1-4K keys 177 / 177 / 183 us, three 2K chunks 316 / 311 / 309)
 constexpr int kNoPage = -1000;   // value exponent of keys that have no page
 constexpr int kFarExp = -60;     // value blocks further below the largest one count as this far
 

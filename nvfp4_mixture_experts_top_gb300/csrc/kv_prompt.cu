@@ -14,7 +14,7 @@
 //               half as long again on the tensor cores.
 // A tile is 512 + 512 cycles of products at D = 128 and 512 of exponentials (a quarter
 // per cycle and scheduler), at once in principle.  Measured, three chunks of 1.5-2.1K
-// tokens after 0.5-4K, 8 heads to one of the cache: 311 us, 735 TFLOP/s, 37% of the
+// tokens after 0.5-4K, 8 heads to one of the cache: 301 us, 759 TFLOP/s, 39% of the
 // rate of a plain bf16 product; DRAM is idle.  What bounds it is the length of the
 // chain softmax, P V, next S of a buffer (about 4900 cycles for two tiles; half of the
 // products or a quarter of the exponentials each take off only 10%), and of its parts
@@ -399,27 +399,35 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
         }
         // weights over the logits, times their values' power of two
 #pragma unroll 1
-        for (int k = 64 * half; k < 64 * half + 64; k += 16) {
-          uint32_t x[16], w[8];
-          tmem_ld16(s_tmem + k, x);
-          const float c = factor(k);
-          const int ve = max(heads.vexp[hd][k >> p.shift] - unit, kFarExp);
-          const float up = kRowBoost - ref + (float)ve;
-          const uint64_t cc = pack2(c, c), uu = pack2(up, up);
-          tmem_ld_wait();
-          uint64_t sum[2] = {0, 0};
+        for (int k = 64 * half; k < 64 * half + 64; k += 32) {
+          uint32_t x[32], w[16];
+          tmem_ld_32x32b_x32(s_tmem + k, x);
+          float c[2], up[2], un[2];
 #pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            float2 y = unpack2(fma2(pack2(__uint_as_float(x[2 * j]), __uint_as_float(x[2 * j + 1])), cc, uu));
-            y.x = ex2(y.x);
-            y.y = ex2(y.y);
-            sum[j & 1] = add2(sum[j & 1], pack2(y.x, y.y));
-            const __half2 z = __floats2half2_rn(y.x, y.y);
-            w[j] = *reinterpret_cast<const uint32_t*>(&z);
+          for (int h = 0; h < 2; ++h) {
+            c[h] = factor(k + 16 * h);
+            const int ve = max(heads.vexp[hd][(k + 16 * h) >> p.shift] - unit, kFarExp);
+            up[h] = kRowBoost - ref + (float)ve;
+            un[h] = exp2_int(-ve);
           }
-          const float2 y = unpack2(add2(sum[0], sum[1]));
-          l = fmaf(y.x + y.y, exp2_int(-ve), l);
-          tmem_st8(s_tmem + 32 * half + (k >> 1), w);
+          tmem_ld_wait();
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const uint64_t cc = pack2(c[h], c[h]), uu = pack2(up[h], up[h]);
+            uint64_t sum[2] = {0, 0};
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+              float2 y = unpack2(fma2(pack2(__uint_as_float(x[16 * h + 2 * j]), __uint_as_float(x[16 * h + 2 * j + 1])), cc, uu));
+              y.x = ex2(y.x);
+              y.y = ex2(y.y);
+              sum[j & 1] = add2(sum[j & 1], pack2(y.x, y.y));
+              const __half2 z = __floats2half2_rn(y.x, y.y);
+              w[8 * h + j] = *reinterpret_cast<const uint32_t*>(&z);
+            }
+            const float2 y = unpack2(add2(sum[0], sum[1]));
+            l = fmaf(y.x + y.y, un[h], l);
+          }
+          tmem_st16(s_tmem + 32 * half + (k >> 1), w);
         }
         tmem_st_wait();
         tc_fence_before();
@@ -489,8 +497,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
         __syncwarp();
       }
       first = false;
-      tc_fence_before();
-      if (!both()) break;  // (both groups' outputs are read)
+      tc_fence_before();  // (the next product over these outputs waits for the weights of all eight warps)
     }
     if (first && tid == 0) p.cut[blockIdx.x].parts = 0;
   }
