@@ -16,8 +16,8 @@
 // per cycle and scheduler), at once in principle.  Measured, three chunks of 1.5-2.1K
 // tokens after 0.5-4K, 8 heads to one of the cache: 301 us, 759 TFLOP/s, 39% of the
 // rate of a plain bf16 product; DRAM is idle.  What bounds it is the length of the
-// chain softmax, P V, next S of a buffer (about 4900 cycles for two tiles; half of the
-// products or a quarter of the exponentials each take off only 10%), and of its parts
+// chain softmax, P V, next S of a buffer (about 4500 cycles for two tiles; with half of
+// the products, or a quarter of the weights, it was 7 or 11% shorter), and of its parts
 // the softmax's instruction issue: 1270 slots per tile and scheduler.  Straight-line
 // code in place of the small loops is slower in each place that was tried (339 -> 347 us
 // with the weights' loop unrolled): warps of five roles share a scheduler's
@@ -332,9 +332,9 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
         if (!wait(&s_full[buf], (gc >> 1) & 1) || !wait(&heads.full[hd], gc / kHeads & 1)) break;
         tc_fence_after();
         const int2 vr = heads.vrange[hd];
-        // the row's logits, 32 keys at a time, twice: for the maximum, then for the
-        // weights.  Loops stay rolled: unrolled, the roles' code outgrew the
-        // instruction cache, and half of all issue slots were lost to it.
+        // the row's logits, twice: for the maximum, then 32 keys at a time for the weights.
+        // Small loops: with all of it unrolled, the roles' code outgrew the instruction
+        // cache, and half of all issue slots were lost to it.
         const int seen = lim - key0;
         const bool odd = key0 + kTile > all_see || vr.x == kNoPage;
         if (odd) {  // keys that the row does not see are -inf
